@@ -6,7 +6,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_size_t, c_void_p
+from ctypes import (POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p)
 
 # AUT_LIB=debug selects the bounds-checked build (libaut_debug.so, built by
 # `python -m audio_encoder_aut_b200.build --debug-bounds`).
@@ -20,6 +20,7 @@ AUT_OK, AUT_ERR_INVALID_ARG, AUT_ERR_UNSUPPORTED, AUT_ERR_WORKSPACE, AUT_ERR_CUD
 
 EPI_BF16, EPI_BF16_GELU, EPI_RESID_F32, EPI_F32 = 0, 1, 2, 3
 LINEAR_FAULT_INJECT, LINEAR_SINGLE_CTA, LINEAR_F16 = 1, 2, 4
+BF16, F16, F32 = 0, 1, 2  # aut_dtype
 
 KERNEL_KINDS = ["upload", "zero_pads", "conv1", "conv2", "conv3", "conv_out", "layernorm",
                 "qkv", "attention", "o_proj", "fc1", "fc2", "proj1", "proj2"]
@@ -54,6 +55,12 @@ class aut_weights(ctypes.Structure):
 class aut_trace(ctypes.Structure):
     _fields_ = [("events", POINTER(c_void_p)), ("capacity", c_int32), ("count", c_int32),
                 ("kinds", POINTER(c_int32))]
+
+
+class aut_head_rows(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("ld_x", c_int64), ("y", c_void_p), ("ld_y", c_int64),
+                ("gamma", c_void_p), ("positions", c_void_p), ("rows", c_int32),
+                ("heads", c_int32)]
 
 
 class AutError(RuntimeError):
@@ -100,6 +107,20 @@ _SIGNATURES = {
     "aut_inject_audio": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32,
                                    c_int32, c_void_p, c_size_t, c_void_p]),
     "aut_inject_workspace_bytes": (c_size_t, [c_int32]),
+    "aut_quantize_rows": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_int32, c_void_p,
+                                    c_void_p, c_void_p]),
+    "aut_linear_i8": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                c_int32, c_int32, c_int32, c_int32, c_void_p, c_int32, c_int32,
+                                c_void_p]),
+    "aut_qk_norm_rope": (c_int32, [POINTER(aut_head_rows), POINTER(aut_head_rows), c_int32,
+                                   c_int32, c_int32, c_int32, c_double, c_int32, c_float,
+                                   c_void_p]),
+    "aut_cross_attention": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
+                                      c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p,
+                                      c_size_t, c_void_p, c_int32, c_void_p]),
+    "aut_cross_attention_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_void_p,
+                                                       c_void_p, c_int32]),
     "aut_check": (c_int32, [c_void_p]),
     "aut_check_status_word": (c_int32, [c_void_p]),
     "aut_status_string": (c_char_p, [c_int32]),
@@ -277,6 +298,57 @@ def aut_inject_audio(embeds: int, token_ids: int, L: int, audio_pad_id: int, aud
 
 def aut_inject_workspace_bytes(L: int) -> int:
     return lib().aut_inject_workspace_bytes(L)
+
+
+def _offsets(values):
+    """(address, entries, owner) of int32 offsets for a call: a contiguous int32 array
+    (numpy's, say) is passed as it is, anything else is copied to one."""
+    face = getattr(values, "__array_interface__", None)
+    if face and face["typestr"] == "<i4" and not face.get("strides") and len(face["shape"]) == 1:
+        return face["data"][0], face["shape"][0], values
+    arr = (c_int32 * max(1, len(values)))(*[int(v) for v in values])
+    return ctypes.addressof(arr), len(values), arr
+
+
+def aut_quantize_rows(x: int, dtype: int, ld_x: int, M: int, K: int, q: int, scale: int,
+                      stream: int) -> int:
+    return lib().aut_quantize_rows(x, dtype, ld_x, M, K, q, scale, stream)
+
+
+def aut_linear_i8(xq: int, x_scale: int, wq: int, w_scale: int, bias: int | None, y: int, M: int,
+                  N: int, K: int, epilogue: int, status: int | None, timeout_ms: int, flags: int,
+                  stream: int) -> int:
+    return lib().aut_linear_i8(xq, x_scale, wq, w_scale, bias, y, M, N, K, epilogue, status,
+                               timeout_ms, flags, stream)
+
+
+def aut_qk_norm_rope(q: aut_head_rows | None, k: aut_head_rows | None, head_dim: int,
+                     x_dtype: int, y_dtype: int, rot_dim: int, theta: float, interleaved: bool,
+                     eps: float, stream: int) -> int:
+    return lib().aut_qk_norm_rope(ctypes.byref(q) if q is not None else None,
+                                  ctypes.byref(k) if k is not None else None, head_dim, x_dtype,
+                                  y_dtype, rot_dim, theta, int(interleaved), eps, stream)
+
+
+def aut_cross_attention(q: int, ld_q: int, k: int, ld_k: int, v: int, ld_v: int, out: int,
+                        ld_out: int, dtype: int, heads_q: int, heads_kv: int, head_dim: int,
+                        cu_q, cu_k, key_mask: int | None, scale: float, workspace: int,
+                        ws_bytes: int, status: int | None, timeout_ms: int, stream: int) -> int:
+    """cu_q and cu_k: offsets of every request's rows, the same number of entries."""
+    (pq, nq, keep_q), (pk, nk, keep_k) = _offsets(cu_q), _offsets(cu_k)
+    if nq != nk or nq < 1:
+        return AUT_ERR_INVALID_ARG
+    return lib().aut_cross_attention(q, ld_q, k, ld_k, v, ld_v, out, ld_out, dtype, heads_q,
+                                     heads_kv, head_dim, pq, pk, nq - 1, key_mask, scale,
+                                     workspace, ws_bytes, status, timeout_ms, stream)
+
+
+def aut_cross_attention_workspace_bytes(heads_q: int, heads_kv: int, head_dim: int, cu_q,
+                                        cu_k) -> int:
+    (pq, nq, keep_q), (pk, nk, keep_k) = _offsets(cu_q), _offsets(cu_k)
+    if nq != nk or nq < 1:
+        return 0
+    return lib().aut_cross_attention_workspace_bytes(heads_q, heads_kv, head_dim, pq, pk, nq - 1)
 
 
 def aut_check(workspace: int) -> int:

@@ -1,0 +1,568 @@
+// Cross attention over an encoder's packed states: the host plan, the kernel for
+// a few query rows, the join of split requests, and the entry point.
+//
+//   out[i, h] = sum_j p_ij v[j, h'] / sum_j p_ij,   p_ij = 2^(s_ij - max_j s_ij),
+//   s_ij = (q[i, h] . k[j, h']) scale log2(e),   h' = h / group
+//
+// over the keys j of query i's request that the mask leaves.  One pass over the
+// keys with the running maximum and sum of the softmax.
+//
+// cross_rows_kernel: 16 rows (query, head of the group) of one request and key
+// head per block.  With so few rows the work is reading keys and values once, so
+// the block's four warps each stream key blocks of their own (block w, w + 4, ...)
+// through a private ring of cp.async copies, with no barrier between warps until
+// their results are joined at the end.  A masked key, or one past the end, is
+// zero-filled by its copy: whatever stands there never enters.  Scores and P V
+// are m16n8k16 products: a tcgen05 tile has 128 rows, and would leave
+// seven eighths of them empty here.
+//
+// A request whose keys take longer than its share of the GPU is split along
+// them; every split leaves its unnormalised rows, their maximum and their sum in
+// the workspace, and cross_join_kernel adds them up in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "aut_cross.h"
+#include "aut_elem.cuh"
+#include "aut_internal.h"
+#include "aut_kernels.h"
+#include "aut_ptx.cuh"
+
+namespace aut {
+namespace {
+
+constexpr int kRows = 16;    // rows of one block
+constexpr int kRowWarps = 4;
+constexpr int kKeys = 32;    // keys of a warp's block: one lane each for the mask
+constexpr int kStages = 3;   // blocks a warp holds in its ring
+
+template <int HD>
+struct RowsCfg {
+    static constexpr int kRowBytes = HD * 2;
+    static constexpr int kTile = kKeys * kRowBytes;  // K or V of one block
+    static constexpr int kWarpBytes = kStages * 2 * kTile;
+    static constexpr int kJoin = kRowWarps * kRows * (HD + 4) * 4;  // the warps' O, padded rows
+    static constexpr int kSmem = kRowWarps * kWarpBytes > kJoin ? kRowWarps * kWarpBytes : kJoin;
+};
+
+// Byte offset of the 16-byte chunk c of row r of a K or V block; the chunks of
+// any 8 consecutive rows at one c fall in different banks (ldmatrix).
+template <int HD>
+AUT_DEV uint32_t row_chunk(int r, int c) {
+    if constexpr (HD >= 64) return r * (HD * 2) + ((c ^ (r & 7)) << 4);
+    if constexpr (HD == 32) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+}
+
+// 16 bytes global -> shared, or 16 zero bytes.
+AUT_DEV void copy16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+AUT_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+AUT_DEV void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+AUT_DEV void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+AUT_DEV void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <typename T>
+AUT_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+AUT_DEV void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                     uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+AUT_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRowWarps * 32)
+    cross_rows_kernel(const __grid_constant__ CrossArgs a) {
+    using Cfg = RowsCfg<HD>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 join_ml[kRowWarps][kRows];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
+    const int seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
+    const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
+    const int nq = nx.q0 - s.q0, nk = nx.k0 - s.k0;
+    const int rows = nq * a.group, tiles = (rows + kRows - 1) / kRows;
+    int item = (int)blockIdx.x - s.item;
+    const int tile = item % tiles;
+    item /= tiles;
+    const int hk = item % a.heads_kv, split = item / a.heads_kv;
+    const int splits = max(1, (nk + a.chunk - 1) / a.chunk);
+    const int key0 = s.k0 + split * a.chunk, key1 = min(nx.k0, key0 + a.chunk);
+    const int n_blocks = (key1 - key0 + kKeys - 1) / kKeys;  // 0 for a request without keys
+
+    // Row r of the tile: query (tile 16 + r) / group, head hk group + (tile 16 + r) % group.
+    auto row_at = [&](int r, int &tok, int &head) {
+        const int i = tile * kRows + r;
+        tok = i / a.group;
+        head = hk * a.group + i - tok * a.group;
+        return i < rows;
+    };
+    const T *kp = static_cast<const T *>(a.k) + hk * HD, *vp = static_cast<const T *>(a.v) + hk * HD;
+    uint8_t *ring = smem + warp * Cfg::kWarpBytes;
+    // Which of block b's keys are read (lane i: key i).
+    auto block_keys = [&](int b) -> uint32_t {
+        const int key = key0 + b * kKeys + lane;
+        const bool in = b < n_blocks && key < key1 && (!a.mask || a.mask[key] != 0);
+        return __ballot_sync(0xffffffffu, in);
+    };
+    constexpr int kChunks = HD / 8;         // 16-byte chunks of a row
+    constexpr int kRowsAtOnce = 32 / kChunks > 0 ? 32 / kChunks : 1;
+    const int cr = lane / kChunks, cc = lane % kChunks;
+    auto copy_block = [&](int b, uint32_t keys, int stage) {
+        const uint32_t dst = smem_addr(ring + stage * 2 * Cfg::kTile);
+        if (keys) {
+#pragma unroll
+            for (int r0 = 0; r0 < kKeys; r0 += kRowsAtOnce) {
+                const int r = r0 + cr;
+                const bool in = (keys >> r) & 1u;
+                const size_t key = in ? (size_t)(key0 + b * kKeys + r) : (size_t)key0;
+                copy16(dst + row_chunk<HD>(r, cc), kp + key * a.ld_k + cc * 8, in);
+                copy16(dst + Cfg::kTile + row_chunk<HD>(r, cc), vp + key * a.ld_v + cc * 8, in);
+            }
+        }
+        copy_commit();
+    };
+
+    // Queries as product operands: rows g and g + 8, columns 16 c + 2 t (+ 8).
+    uint32_t qf[HD / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int tok, head;
+        const bool in = row_at(g + 8 * i, tok, head);
+        const T *qp = static_cast<const T *>(a.q) + (size_t)(s.q0 + (in ? tok : 0)) * a.ld_q + head * HD;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) {
+            qf[c][i] = in ? *reinterpret_cast<const uint32_t *>(qp + 16 * c + 2 * t) : 0u;
+            qf[c][2 + i] = in ? *reinterpret_cast<const uint32_t *>(qp + 16 * c + 2 * t + 8) : 0u;
+        }
+    }
+    float o[HD / 8][4];
+#pragma unroll
+    for (int c = 0; c < HD / 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8; l: this lane's share
+
+    uint32_t keys[kStages];  // of the blocks in the ring
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        keys[i] = block_keys(warp + i * kRowWarps);
+        copy_block(warp + i * kRowWarps, keys[i], i);
+    }
+    uint32_t ahead = block_keys(warp + (kStages - 1) * kRowWarps);
+    int stage = 0;
+    for (int b = warp; b < n_blocks; b += kRowWarps) {
+        {  // the block kStages - 1 ahead, into the stage the previous step has read
+            const int fill = stage == 0 ? kStages - 1 : stage - 1;
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (i == fill) keys[i] = ahead;
+            copy_block(b + (kStages - 1) * kRowWarps, ahead, fill);
+            ahead = block_keys(b + kStages * kRowWarps);
+        }
+        copy_wait<kStages - 1>();
+        __syncwarp();
+        uint32_t live = 0;
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (i == stage) live = keys[i];
+        const uint32_t ks = smem_addr(ring + stage * 2 * Cfg::kTile), vs = ks + Cfg::kTile;
+        if (live) {
+            // S: 16 rows x 32 keys, four tiles of 8 keys.
+            float sc[kKeys / 8][4];
+#pragma unroll
+            for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kKeys / 8; j += 2)
+#pragma unroll
+                for (int c = 0; c < HD / 16; ++c) {
+                    uint32_t kf[4];  // keys 8 j .. (chunks 2 c, 2 c + 1), keys 8 j + 8 .. (the same)
+                    ldmatrix4(ks + row_chunk<HD>(8 * j + (lane & 7) + (lane >> 4) * 8,
+                                                 2 * c + ((lane >> 3) & 1)),
+                              kf);
+                    mma16816<T>(sc[j], qf[c], kf[0], kf[1]);
+                    mma16816<T>(sc[j + 1], qf[c], kf[2], kf[3]);
+                }
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = (live >> (8 * j + 2 * t + (e & 1))) & 1u;
+                    sc[j][e] = in ? sc[j][e] * a.scale_log2e : -INFINITY;
+                    top[e >> 1] = fmaxf(top[e >> 1], sc[j][e]);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+                const float mn = fmaxf(m[i], top[i]);
+                // No finite score yet: 2^(-inf - 0) = 0 keeps sums and rows at zero.
+                const float base = mn == -INFINITY ? 0.f : mn;
+                const float shrink = ex2_approx(m[i] - base);
+                m[i] = mn;
+                l[i] *= shrink;
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c) {
+                    o[c][2 * i] *= shrink;
+                    o[c][2 * i + 1] *= shrink;
+                }
+#pragma unroll
+                for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sc[j][2 * i + e] = ex2_approx(sc[j][2 * i + e] - base);
+                        l[i] += sc[j][2 * i + e];
+                    }
+            }
+            // O += P V.  P in 16 bits: in [0, 1], off by half a step of its type,
+            // the same rounding the output gets once more.
+#pragma unroll
+            for (int j = 0; j < kKeys / 16; ++j) {
+                const uint32_t pf[4] = {pack2<T>(sc[2 * j][0], sc[2 * j][1]),
+                                        pack2<T>(sc[2 * j][2], sc[2 * j][3]),
+                                        pack2<T>(sc[2 * j + 1][0], sc[2 * j + 1][1]),
+                                        pack2<T>(sc[2 * j + 1][2], sc[2 * j + 1][3])};
+#pragma unroll
+                for (int c = 0; c < HD / 16; ++c) {
+                    uint32_t vf[4];  // chunk 2 c (keys 16 j, 16 j + 8), chunk 2 c + 1 (the same)
+                    ldmatrix4_trans(vs + row_chunk<HD>(16 * j + (lane & 15), 2 * c + (lane >> 4)), vf);
+                    mma16816<T>(o[2 * c], pf, vf[0], vf[1]);
+                    mma16816<T>(o[2 * c + 1], pf, vf[2], vf[3]);
+                }
+            }
+        }
+        __syncwarp();  // every lane has read the stage before it is filled again
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    __syncthreads();  // every warp is done with its ring; the join reuses it
+
+    constexpr int kLd = HD + 4;
+    float *join = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (t == 0) join_ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int c = 0; c < HD / 8; ++c)
+            *reinterpret_cast<float2 *>(join + (warp * kRows + g + 8 * i) * kLd + 8 * c + 2 * t) =
+                make_float2(o[c][2 * i], o[c][2 * i + 1]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * (HD / 8); i += kRowWarps * 32) {
+        const int r = i / (HD / 8), c = i % (HD / 8);
+        int tok, head;
+        if (!row_at(r, tok, head)) continue;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, join_ml[w][r].x);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f, v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+            const float f = ex2_approx(join_ml[w][r].x - base);
+            sum = fmaf(f, join_ml[w][r].y, sum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(f, join[(w * kRows + r) * kLd + 8 * c + e], v[e]);
+        }
+        if (splits > 1) {
+            const size_t row = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
+            store8(a.part_o + row * HD + 8 * c, v);
+            if (c == 0) a.part_ml[row] = make_float2(mx, sum);
+        } else {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            store8(static_cast<T *>(a.out) + (size_t)(s.q0 + tok) * a.ld_out + head * HD + 8 * c, v);
+        }
+    }
+}
+
+// Adds the splits of every row of the split requests: a warp per row, HD / 8
+// lanes of it with 8 columns each.
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ CrossArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int kLanes = HD / 8, kRowsAtOnce = 32 / kLanes;
+    const int warp = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
+    const int first = warp * kRowsAtOnce;
+    if (first >= a.items) return;
+    // Each lane's row may belong to another request than the warp's first.
+    int seq = cross_find(seqs, a.n_seq, first, lane);
+    const int item = first + lane / kLanes, c = lane % kLanes;
+    if (item >= a.items) return;
+    while (seqs[seq + 1].item <= item) ++seq;
+    const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
+    const int nq = nx.q0 - s.q0, splits = (nx.k0 - s.k0 + a.chunk - 1) / a.chunk;
+    const int r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
+    const size_t step = (size_t)nq * a.heads_q, row0 = (size_t)s.part + r;
+    float mx = -INFINITY;
+    for (int i = 0; i < splits; ++i) mx = fmaxf(mx, a.part_ml[row0 + i * step].x);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {
+        const float2 ml = a.part_ml[row0 + i * step];
+        float w[8];
+        load8(a.part_o + (row0 + i * step) * HD + 8 * c, w);
+        const float f = ex2_approx(ml.x - base);
+        sum = fmaf(f, ml.y, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(f, w[e], v[e]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= inv;
+    store8(static_cast<T *>(a.out) + (size_t)(s.q0 + tok) * a.ld_out + head * HD + 8 * c, v);
+}
+
+// -------------------------------------------------------------------- plan --
+
+// Blocks the splits aim for, and the fewest keys worth a split of their own.
+constexpr int kTargetItems = 2 * 148;
+constexpr int kMinChunk = 512;
+
+struct CrossPlan {
+    int64_t items = 0;      // row-kernel items
+    int64_t join_rows = 0;  // rows of split requests
+    int64_t part_rows = 0;  // partial rows
+    int chunk = kMinChunk;
+};
+
+bool head_dim_ok(int hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
+
+aut_status check_shape(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
+                       int n_seq) {
+    if (heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv || n_seq < 0 || !cu_q || !cu_k)
+        return AUT_ERR_INVALID_ARG;
+    if (!head_dim_ok(hd)) return AUT_ERR_UNSUPPORTED;
+    if (heads_q > (1 << 20) / hd) return AUT_ERR_UNSUPPORTED;
+    if (cu_q[0] != 0 || cu_k[0] != 0) return AUT_ERR_INVALID_ARG;
+    for (int i = 0; i < n_seq; ++i)
+        if (cu_q[i + 1] < cu_q[i] || cu_k[i + 1] < cu_k[i]) return AUT_ERR_INVALID_ARG;
+    // Row indexes (query, head of a group) are 32-bit in the kernels.
+    if ((int64_t)cu_q[n_seq] * heads_q > 0x7fffffffll) return AUT_ERR_UNSUPPORTED;
+    return AUT_OK;
+}
+
+int64_t row_tiles(int64_t nq, int group) { return (nq * group + kRows - 1) / kRows; }
+
+aut_status plan_cross(int heads_q, int heads_kv, const int32_t *cu_q, const int32_t *cu_k,
+                      int n_seq, CrossPlan *p) {
+    const int group = heads_q / heads_kv;
+    int64_t work = 0;  // keys read by all items, unsplit
+    for (int i = 0; i < n_seq; ++i)
+        work += row_tiles(cu_q[i + 1] - cu_q[i], group) * heads_kv * (cu_k[i + 1] - cu_k[i]);
+    // Every split about as long as the GPU's share of the whole.
+    const int64_t share = (work + kTargetItems - 1) / kTargetItems;
+    p->chunk = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk), 1 << 30);
+    p->chunk = (p->chunk + kKeys - 1) / kKeys * kKeys;
+    for (int i = 0; i < n_seq; ++i) {
+        const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
+        if (nq == 0) continue;
+        const int64_t splits = std::max<int64_t>(1, (nk + p->chunk - 1) / p->chunk);
+        p->items += row_tiles(nq, group) * heads_kv * splits;
+        if (splits > 1) {
+            p->join_rows += nq * heads_q;
+            p->part_rows += nq * heads_q * splits;
+        }
+    }
+    if (p->items > 0x7fffffffll || p->join_rows > 0x7fffffffll || p->part_rows > 0x7fffffffll)
+        return AUT_ERR_UNSUPPORTED;
+    return AUT_OK;
+}
+
+// The requests as the row kernel (join = false) or the join sees them.
+void fill_seqs(CrossSeq *out, bool join, const CrossPlan &p, int heads_q, int heads_kv,
+               const int32_t *cu_q, const int32_t *cu_k, int n_seq) {
+    int64_t item = 0, part = 0;
+    for (int i = 0; i <= n_seq; ++i) {
+        out[i] = {cu_q[i], cu_k[i], (int)item, (int)part};
+        if (i == n_seq) break;
+        const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
+        if (nq == 0) continue;
+        const int64_t splits = std::max<int64_t>(1, (nk + p.chunk - 1) / p.chunk);
+        if (!join)
+            item += row_tiles(nq, heads_q / heads_kv) * heads_kv * splits;
+        else if (splits > 1)
+            item += nq * heads_q;
+        if (splits > 1) part += nq * heads_q * splits;
+    }
+}
+
+struct CrossLayout {
+    size_t rows, join, part_o, part_ml, total;
+};
+CrossLayout cross_layout(const CrossPlan &p, int hd, int n_seq) {
+    CrossLayout l{};
+    size_t off = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    const size_t list = n_seq > kCrossInline ? (size_t)(n_seq + 1) * sizeof(CrossSeq) : 0;
+    l.rows = take(list);
+    l.join = take(list);
+    l.part_o = take((size_t)p.part_rows * hd * 4);
+    l.part_ml = take((size_t)p.part_rows * 8);
+    l.total = std::max<size_t>(off, 256);
+    return l;
+}
+
+template <typename T, int HD>
+cudaError_t launch_rows(const CrossArgs &a, cudaStream_t st) {
+    constexpr int smem = RowsCfg<HD>::kSmem;
+    const cudaError_t e = smem_attr_once<cross_rows_kernel<T, HD>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cross_rows_kernel<T, HD>, dim3(a.items), dim3(kRowWarps * 32), smem, st, 1, a);
+}
+
+template <typename T, int HD>
+cudaError_t launch_join(const CrossArgs &a, cudaStream_t st) {
+    constexpr int rows_a_block = 8 * (32 / (HD / 8));
+    return launch_pdl(cross_join_kernel<T, HD>, dim3((unsigned)((a.items + (int64_t)rows_a_block - 1) / rows_a_block)),
+                      dim3(256), 0, st, 1, a);
+}
+
+template <typename T>
+cudaError_t launch_kernel(bool join, int hd, const CrossArgs &a, cudaStream_t st) {
+    switch (hd) {
+        case 16: return join ? launch_join<T, 16>(a, st) : launch_rows<T, 16>(a, st);
+        case 32: return join ? launch_join<T, 32>(a, st) : launch_rows<T, 32>(a, st);
+        case 64: return join ? launch_join<T, 64>(a, st) : launch_rows<T, 64>(a, st);
+        default: return join ? launch_join<T, 128>(a, st) : launch_rows<T, 128>(a, st);
+    }
+}
+
+}  // namespace
+}  // namespace aut
+
+using namespace aut;
+
+extern "C" size_t aut_cross_attention_workspace_bytes(int32_t heads_q, int32_t heads_kv,
+                                                      int32_t head_dim, const int32_t *cu_q,
+                                                      const int32_t *cu_k, int32_t n_seq) {
+    CrossPlan p;
+    if (check_shape(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq) != AUT_OK ||
+        plan_cross(heads_q, heads_kv, cu_q, cu_k, n_seq, &p) != AUT_OK)
+        return 0;
+    return cross_layout(p, head_dim, n_seq).total;
+}
+
+extern "C" aut_status aut_cross_attention(
+    const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+    void *out, int64_t ld_out, int32_t dtype, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+    const int32_t *cu_q, const int32_t *cu_k, int32_t n_seq, const uint8_t *key_mask, float scale,
+    void *workspace, size_t ws_bytes, int32_t *status, int32_t timeout_ms, aut_stream_t stream) {
+    aut_status st = check_shape(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
+    if (st != AUT_OK) return st;
+    if ((dtype != AUT_BF16 && dtype != AUT_F16) || timeout_ms < 0 || !(scale > 0.f) ||
+        !std::isfinite(scale))
+        return AUT_ERR_INVALID_ARG;
+    const int64_t tq = cu_q[n_seq], tk = cu_k[n_seq], most = (int64_t)1 << 38;
+    const int64_t wq = (int64_t)heads_q * head_dim, wk = (int64_t)heads_kv * head_dim;
+    if (tq > 0 && (!q || !out || ld_q < wq || ld_out < wq || ld_q > most || ld_out > most ||
+                   ld_q % 8 || ld_out % 8))
+        return AUT_ERR_INVALID_ARG;
+    if (tk > 0 && (!k || !v || ld_k < wk || ld_v < wk || ld_k > most || ld_v > most || ld_k % 8 ||
+                   ld_v % 8))
+        return AUT_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+         reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(out)) & 15u)
+        return AUT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(status) & 3u) return AUT_ERR_INVALID_ARG;
+    CrossPlan p;
+    st = plan_cross(heads_q, heads_kv, cu_q, cu_k, n_seq, &p);
+    if (st != AUT_OK) return st;
+    const CrossLayout lay = cross_layout(p, head_dim, n_seq);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return AUT_ERR_INVALID_ARG;
+    if (ws_bytes < lay.total) return AUT_ERR_WORKSPACE;
+    if (tq == 0) return AUT_OK;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    CrossArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.mask = key_mask;
+    a.ld_q = ld_q;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.ld_out = ld_out;
+    a.heads_q = heads_q;
+    a.heads_kv = heads_kv;
+    a.group = heads_q / heads_kv;
+    a.scale_log2e = (float)((double)scale * 1.4426950408889634);
+    a.chunk = p.chunk;
+    a.n_seq = n_seq;
+    a.part_o = reinterpret_cast<float *>(ws + lay.part_o);
+    a.part_ml = reinterpret_cast<float2 *>(ws + lay.part_ml);
+    const bool listed = n_seq > kCrossInline;
+    CrossSeq *list = listed ? new (std::nothrow) CrossSeq[n_seq + 1] : a.inline_seqs;
+    if (!list) return AUT_ERR_WORKSPACE;
+    aut_status result = AUT_OK;
+    for (int join = 0; join < (p.join_rows > 0 ? 2 : 1) && result == AUT_OK; ++join) {
+        a.items = (int)(join ? p.join_rows : p.items);
+        fill_seqs(list, join != 0, p, heads_q, heads_kv, cu_q, cu_k, n_seq);
+        a.seqs = nullptr;
+        if (listed) {
+            CrossSeq *dev = reinterpret_cast<CrossSeq *>(ws + (join ? lay.join : lay.rows));
+            a.seqs = dev;
+            if (launch_upload(reinterpret_cast<const int32_t *>(list), (size_t)(n_seq + 1) * 4,
+                              reinterpret_cast<int32_t *>(dev), s) != cudaSuccess)
+                result = AUT_ERR_CUDA;
+        }
+        if (result == AUT_OK &&
+            (dtype == AUT_BF16 ? launch_kernel<__nv_bfloat16>(join != 0, head_dim, a, s)
+                               : launch_kernel<__half>(join != 0, head_dim, a, s)) != cudaSuccess)
+            result = AUT_ERR_CUDA;
+    }
+    if (listed) delete[] list;
+    return result;
+}

@@ -78,16 +78,16 @@ int sm_count() { return sm_count_cached(); }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int BN, int CG>
+template <int BN, int CG, bool I8 = false>
 GemmStatus run(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc,
                const GemmArgs &args,
                cudaStream_t st) {
     using Cfg = GemmCfg<BN, CG>;
-    if (smem_attr_once<gemm_tc_kernel<BN, CG>>(Cfg::SMEM_BYTES) != cudaSuccess)
+    if (smem_attr_once<gemm_tc_kernel<BN, CG, I8>>(Cfg::SMEM_BYTES) != cudaSuccess)
         return GemmStatus::kLaunch;
     const int tiles = args.num_m_tiles * args.num_n_tiles;
     const int groups = std::min(tiles, sm_count() / CG);
-    const cudaError_t e = launch_pdl(gemm_tc_kernel<BN, CG>, dim3(groups * CG), dim3(kGemmThreads),
+    const cudaError_t e = launch_pdl(gemm_tc_kernel<BN, CG, I8>, dim3(groups * CG), dim3(kGemmThreads),
                                      Cfg::SMEM_BYTES, st, CG, ta, tb, tc, args);
     return e == cudaSuccess ? GemmStatus::kOk : GemmStatus::kLaunch;
 }
@@ -114,6 +114,27 @@ GemmStatus dispatch(int bn, int cg, const CUtensorMap &ta, const CUtensorMap &tb
         case 192: return run<192, 1>(ta, tb, tc, args, st);
         case 240: return run<240, 1>(ta, tb, tc, args, st);
         case 256: return run<256, 1>(ta, tb, tc, args, st);
+        default: return GemmStatus::kBadShape;
+    }
+}
+
+// The widths choose_tile picks from, with 8-bit operands.
+GemmStatus dispatch_i8(int bn, int cg, const CUtensorMap &ta, const CUtensorMap &tb,
+                       const CUtensorMap &tc, const GemmArgs &args, cudaStream_t st) {
+    if (cg == 2) {
+        switch (bn) {
+            case 64: return run<64, 2, true>(ta, tb, tc, args, st);
+            case 128: return run<128, 2, true>(ta, tb, tc, args, st);
+            case 256: return run<256, 2, true>(ta, tb, tc, args, st);
+            default: return GemmStatus::kBadShape;
+        }
+    }
+    switch (bn) {
+        case 16: return run<16, 1, true>(ta, tb, tc, args, st);
+        case 32: return run<32, 1, true>(ta, tb, tc, args, st);
+        case 64: return run<64, 1, true>(ta, tb, tc, args, st);
+        case 128: return run<128, 1, true>(ta, tb, tc, args, st);
+        case 256: return run<256, 1, true>(ta, tb, tc, args, st);
         default: return GemmStatus::kBadShape;
     }
 }
@@ -153,8 +174,10 @@ void choose_tile(int M, int N, int sms, bool allow_pair, int *bn_out, int *cg_ou
 
 GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st) {
     if (L.M <= 0) return GemmStatus::kOk;
-    if (L.N <= 0 || L.K <= 0 || L.K % 64 || L.N % 16 || !L.a || !L.w || !L.out)
+    const bool i8 = L.x_scale != nullptr;
+    if (L.N <= 0 || L.K <= 0 || L.K % (i8 ? 16 : 64) || L.N % 16 || !L.a || !L.w || !L.out)
         return GemmStatus::kBadShape;
+    if (i8 && (!L.w_scale || !aligned16(L.w_scale))) return GemmStatus::kBadShape;
     if (!aligned16(L.a) || !aligned16(L.w) || !aligned16(L.out) || (L.bias && !aligned16(L.bias)))
         return GemmStatus::kBadShape;
     int bn = 0, cg = 1;
@@ -162,13 +185,17 @@ GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st) {
     if (!bn) return GemmStatus::kBadShape;
     CUtensorMap ta, tb;
     const cuuint64_t da[2] = {(cuuint64_t)L.K, (cuuint64_t)L.M};
-    const cuuint64_t sa[1] = {(cuuint64_t)L.K * 2};
-    const cuuint32_t ba[2] = {64, 128};
+    const cuuint32_t kel = i8 ? 128 : 64;  // K elements of a k-block: 128 bytes
+    const cuuint64_t sa[1] = {(cuuint64_t)L.K * (i8 ? 1 : 2)};
+    const cuuint32_t ba[2] = {kel, 128};
     const cuuint64_t db[2] = {(cuuint64_t)L.K, (cuuint64_t)L.N};
-    const cuuint32_t bb[2] = {64, (cuuint32_t)(bn / cg)};
+    const cuuint32_t bb[2] = {kel, (cuuint32_t)(bn / cg)};
     // fp16 operands use the same maps: the copies move bytes, and the zero fill
-    // of out-of-range rows is zero in both types.
-    if (!make_map(&ta, 2, L.a, da, sa, ba) || !make_map(&tb, 2, L.w, db, sa, bb))
+    // of out-of-range rows (and, for 8-bit operands, of the last k-block's
+    // columns past K) is zero in every type.
+    const CUtensorMapDataType op =
+        i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_map(&ta, 2, L.a, da, sa, ba, op) || !make_map(&tb, 2, L.w, db, sa, bb, op))
         return GemmStatus::kTensorMap;
     GemmArgs args{};
     args.f16 = L.f16 ? 1 : 0;
@@ -177,7 +204,9 @@ GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st) {
     args.N = L.N;
     args.num_m_tiles = (L.M + 128 * cg - 1) / (128 * cg);
     args.num_n_tiles = L.N / bn;
-    args.num_k_blocks = L.K / 64;
+    args.num_k_blocks = (L.K + (int)kel - 1) / (int)kel;
+    args.x_scale = L.x_scale;
+    args.w_scale = L.w_scale;
     args.conv = 0;
     args.epi = L.epi;
     args.bias = static_cast<const __nv_bfloat16 *>(L.bias);
@@ -206,7 +235,7 @@ GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st) {
             return GemmStatus::kTensorMap;
         args.tma_out = 1;
     }
-    return dispatch(bn, cg, ta, tb, tc, args, st);
+    return i8 ? dispatch_i8(bn, cg, ta, tb, tc, args, st) : dispatch(bn, cg, ta, tb, tc, args, st);
 }
 
 GemmStatus launch_conv_gemm(const ConvLaunch &L, cudaStream_t st) {

@@ -9,7 +9,11 @@
 //     previous conv's output, so TMA loads it directly (no im2col buffer);
 //   - conv_out, whose epilogue adds the chunk's sinusoid row, drops the tokens
 //     past the chunk's valid length and writes each kept row to its packed
-//     position (token packing fused into the GEMM).
+//     position (token packing fused into the GEMM);
+//   - the 8-bit linear layers (I8): int8 operands, exact int32 sums in tensor
+//     memory, scaled by row and by column on the way out.  A k-block is still
+//     128 bytes of K (128 elements, K = 32 per MMA), so the ring, the swizzle
+//     and the MMA count per k-block are those of bf16 at twice its products.
 //
 // Block = 10 warps: warp 0 issues TMA loads into a STAGES-deep shared-memory
 // ring, warp 1 owns the tensor-memory allocation and issues tcgen05.mma from
@@ -68,6 +72,8 @@ struct GemmArgs {
     // bf16 epilogues: output columns from here on are written as fp16 instead
     // (the V part of qkv for the tensor-core attention); a multiple of 64.
     int f16_col;
+    // I8: Y = acc x_scale[m] w_scale[n] before the rest of the epilogue.
+    const float *x_scale, *w_scale;
 };
 
 // BN: tile width of one MMA (N).  CG: CTAs per MMA (1, or 2 for a CTA pair
@@ -169,12 +175,27 @@ AUT_DEV void add_bias16(float (&v)[16], const __nv_bfloat16 *bias, int n0) {
     }
 }
 
-template <int BN, int CG>
+// 16 int32 accumulator columns (as tcgen05.ld returns their bits) to fp32, times
+// the row's scale and each column's.
+AUT_DEV void scale_i8x16(float (&v)[16], float sx, const float *w_scale, int n0) {
+    const float4 *wp = reinterpret_cast<const float4 *>(w_scale + n0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float4 w = __ldg(wp + q);
+        v[4 * q] = __int2float_rn(__float_as_int(v[4 * q])) * sx * w.x;
+        v[4 * q + 1] = __int2float_rn(__float_as_int(v[4 * q + 1])) * sx * w.y;
+        v[4 * q + 2] = __int2float_rn(__float_as_int(v[4 * q + 2])) * sx * w.z;
+        v[4 * q + 3] = __int2float_rn(__float_as_int(v[4 * q + 3])) * sx * w.w;
+    }
+}
+
+template <int BN, int CG, bool I8>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const GemmArgs args) {
     using Cfg = GemmCfg<BN, CG>;
     constexpr int STAGES = Cfg::STAGES;
+    constexpr int KEL = I8 ? 128 : 64;  // K elements of a k-block (128 bytes)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -263,9 +284,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const int row = b_row + h * Cfg::MMA_N;
                     if (!args.conv) {
                         if constexpr (CG == 2)
-                            tma_load_2d_pair(b_dst, &tmB, map_to_rank(full + stage, 0), kb * 64, row);
+                            tma_load_2d_pair(b_dst, &tmB, map_to_rank(full + stage, 0), kb * KEL, row);
                         else
-                            tma_load_2d(b_dst, &tmB, full + stage, kb * 64, row);
+                            tma_load_2d(b_dst, &tmB, full + stage, kb * KEL, row);
                     } else {
                         const int tap = kb / args.conv_cblocks;
                         const int cb = kb - tap * args.conv_cblocks;
@@ -282,10 +303,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 uint8_t *a_dst = sA + stage * Cfg::A_BYTES;
                 if (!args.conv) {
                     if constexpr (CG == 2)
-                        tma_load_2d_pair(a_dst, &tmA, map_to_rank(full + stage, 0), kb * 64,
+                        tma_load_2d_pair(a_dst, &tmA, map_to_rank(full + stage, 0), kb * KEL,
                                          m_slot * 128);
                     else
-                        tma_load_2d(a_dst, &tmA, full + stage, kb * 64, m_slot * 128);
+                        tma_load_2d(a_dst, &tmA, full + stage, kb * KEL, m_slot * 128);
                 } else {
                     const int tap = kb / args.conv_cblocks;
                     const int cb = kb - tap * args.conv_cblocks;
@@ -385,7 +406,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             // -------------------------------------------------- MMA issuer --
-            const uint32_t idesc = args.f16 ? idesc_f16_f32(128 * CG, Cfg::MMA_N)
+            const uint32_t idesc = I8         ? idesc_i8_s32(128 * CG, Cfg::MMA_N)
+                                   : args.f16 ? idesc_f16_f32(128 * CG, Cfg::MMA_N)
                                             : idesc_bf16_f32(128 * CG, Cfg::MMA_N);
             constexpr uint16_t kPair = 0x3;
             int stage = 0, it = 0;
@@ -426,7 +448,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         for (int kk = 0; kk < 4; ++kk) {  // K = 16 per MMA: +32 bytes in the row
                             if (kk >= ksteps) break;
                             const uint32_t accumulate = (kb | kk) != 0;
-                            if constexpr (CG == 2)
+                            if constexpr (I8 && CG == 2)
+                                tc_mma_i8_pair(d, a_desc + 2 * kk, b_desc + 2 * kk, idesc,
+                                               accumulate);
+                            else if constexpr (I8)
+                                tc_mma_i8(d, a_desc + 2 * kk, b_desc + 2 * kk, idesc, accumulate);
+                            else if constexpr (CG == 2)
                                 tc_mma_bf16_pair(d, a_desc + 2 * kk, b_desc + 2 * kk, idesc,
                                                  accumulate);
                             else
@@ -615,6 +642,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int m0 = ((tile / args.num_n_tiles) * CG + (int)rank) * 128 + quad * 32;
             const bool slab = m0 < args.M;  // warp-uniform
             const int n_first = (tile % args.num_n_tiles) * BN + half * HW;
+            float sx = 0.f;  // I8: this row's scale
+            if constexpr (I8) sx = m0 + lane < args.M ? __ldg(args.x_scale + m0 + lane) : 0.f;
             const uint32_t t_res = tmem_base + ((uint32_t)(quad * 32) << 16) + BN + half * HW;
             t_acc += half * HW;
 #pragma unroll 1
@@ -630,6 +659,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         tmem_ld16(t_res + p * pcols, r[0]);
                         tmem_ld16(t_res + p * pcols + 16, r[1]);
                         tc_wait_ld();
+                        if constexpr (I8) {
+                            scale_i8x16(v[0], sx, args.w_scale, n_first + p * pcols);
+                            scale_i8x16(v[1], sx, args.w_scale, n_first + p * pcols + 16);
+                        }
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -638,6 +671,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (resid_drain && slab && p > 0 && lane == 0) load_x(tile, p * pcols, stg);
                         __syncwarp();  // the warp-wide TMEM wait needs every lane here
                         tc_wait_ld();
+                        if constexpr (I8) {
+                            scale_i8x16(v[0], sx, args.w_scale, n_first + p * pcols);
+                            scale_i8x16(v[1], sx, args.w_scale, n_first + p * pcols + 16);
+                        }
                         if (!resid) {
                             add_bias16(v[0], args.bias, n_first + p * pcols);
                             add_bias16(v[1], args.bias, n_first + p * pcols + 16);
@@ -686,6 +723,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         tc_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
+                            if constexpr (I8)
+                                scale_i8x16(v[i], sx, args.w_scale,
+                                            n_first + p * pcols + 32 * h + 16 * i);
                             add_bias16(v[i], args.bias, n_first + p * pcols + 32 * h + 16 * i);
                             if (args.epi == kEpiBf16Gelu) {
 #pragma unroll
@@ -766,6 +806,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const int n0 = n_blk * BN + (k ? c1 : c0) * 16;
                     const size_t end = dst_row + n0 + (args.epi == kEpiBf16GeluSplit ? args.N : 0) + 16;
                     if (!AUT_IN_BOUNDS(end <= args.out_elems, args.status)) continue;
+                    if constexpr (I8)
+                        scale_i8x16(v, __ldg(args.x_scale + ((tile / args.num_n_tiles) * CG + (int)rank) * 128 + r),
+                                    args.w_scale, n0);
                     if (!resid) add_bias16(v, args.bias, n0);
                     switch (args.epi) {
                         case kEpiBf16:

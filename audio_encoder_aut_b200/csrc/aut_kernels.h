@@ -151,6 +151,9 @@ struct LinearLaunch {
     bool single_cta = false;  // force one CTA per MMA (no CTA pairs)
     bool f16 = false;         // A and W are fp16 instead of bf16
     int f16_col = 1 << 30;    // kEpiBf16: output columns from here on written as fp16
+    // 8-bit operands: a int8 [M, K] with x_scale fp32 [M], w int8 [N, K] with
+    // w_scale fp32 [N]; K a multiple of 16.  Both null: bf16 or fp16 operands.
+    const float *x_scale = nullptr, *w_scale = nullptr;
 };
 GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st);
 

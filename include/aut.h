@@ -328,6 +328,104 @@ aut_status aut_inject_audio(void *embeds, const int32_t *token_ids, int32_t L,
 /* No passage: a library helper.  Bytes of device workspace aut_inject_audio needs. */
 size_t aut_inject_workspace_bytes(int32_t L);
 
+/* ---- The decoder's side of the encoder's states ----
+ * Operators that a decoder layer runs over the packed states aut_encode leaves
+ * (or over its own tokens): projections in 8-bit integers, the norm and
+ * rotation of query and key heads, and attention to the states.  Conventions
+ * are the file's; strides (ld_*) count elements from one row to the next. */
+
+/* Element types. */
+typedef enum { AUT_BF16 = 0, AUT_F16 = 1, AUT_F32 = 2 } aut_dtype;
+
+/* No passage: a library operator.  Rows to 8-bit integers with a scale each:
+ * scale[m] = max_k |x[m, k]| / 127 and q[m, k] = x[m, k] / scale[m] rounded to
+ * nearest even, both in fp32 (IEEE division), so x ~ scale[m] q[m, k].  A row
+ * of zeros gets scale 0 and zeros; a row that holds an infinity or NaN gets
+ * that as its scale and zeros, which aut_linear_i8 turns into a row of NaN.
+ * x: device, `dtype` (aut_dtype) [M, K] with row stride ld_x >= K, rows 16-byte
+ * aligned; q: device int8 [M, K], 16-byte aligned; scale: device fp32 [M].
+ * K a multiple of 16, at most 131072.  Weights [N, K] are quantised per
+ * channel by the same call. */
+aut_status aut_quantize_rows(const void *x, int32_t dtype, int64_t ld_x, int32_t M, int32_t K,
+                             void *q, void *scale, aut_stream_t stream);
+
+/* No passage: a library operator.  A linear layer in 8-bit integers,
+ * Y = (Xq Wq^T) x_scale[m] w_scale[n] + b, the products summed exactly in int32.
+ * xq: device int8 [M, K]; x_scale: device fp32 [M]; wq: device int8 [N, K];
+ * w_scale: device fp32 [N]; bias: device bf16 [N] or NULL; xq, wq, w_scale,
+ * bias and y 16-byte aligned.  epilogue, status, timeout_ms and flags as for
+ * aut_linear (AUT_LINEAR_F16 is refused); the GELU and the residual add work on
+ * the scaled sum.  K a multiple of 16, at most 131072 (so that no sum passes
+ * int32), N a multiple of 16.  At most 32 rows run on a kernel without
+ * pipeline waits, which ignores AUT_LINEAR_SINGLE_CTA and refuses
+ * AUT_LINEAR_FAULT_INJECT (AUT_ERR_UNSUPPORTED). */
+aut_status aut_linear_i8(const void *xq, const void *x_scale, const void *wq, const void *w_scale,
+                         const void *bias, void *y, int32_t M, int32_t N, int32_t K,
+                         int32_t epilogue, int32_t *status, int32_t timeout_ms, int32_t flags,
+                         aut_stream_t stream);
+
+/* The heads of one side (queries or keys) for aut_qk_norm_rope: row r, head h
+ * is x[r * ld_x + h * head_dim ...].  gamma: device bf16 [head_dim], or NULL for
+ * a gain of one; positions: device int32 [rows] (any sign), or NULL for no
+ * rotation of this side.  y may be x with the same stride and type (in place);
+ * otherwise the two must not overlap. */
+typedef struct {
+    const void *x;
+    int64_t ld_x;
+    void *y;
+    int64_t ld_y;
+    const void *gamma;
+    const int32_t *positions;
+    int32_t rows, heads;
+} aut_head_rows;
+
+/* No passage: a library operator.  RMS norm of every query and key head, then
+ * the rotation by position, in one pass: x <- x / sqrt(mean x^2 + eps) * gamma
+ * over head_dim; pair i < rot_dim / 2 of the head, (x[i], x[i + rot_dim / 2]), or
+ * (x[2 i], x[2 i + 1]) with `interleaved`, turns by the angle
+ * position * theta^(-2 i / rot_dim); elements from rot_dim on are normed only.
+ * The angle is reduced exactly, whatever the position.  q and k (either may
+ * be NULL) may have different numbers of rows and heads; x of both is
+ * `x_dtype`, y `y_dtype` (aut_dtype), rows 16-byte aligned.  head_dim one of 16, 32,
+ * 64, 128, 256; rot_dim a multiple of 16 in [0, head_dim]; theta >= 1. */
+aut_status aut_qk_norm_rope(const aut_head_rows *q, const aut_head_rows *k, int32_t head_dim,
+                            int32_t x_dtype, int32_t y_dtype, int32_t rot_dim, double theta,
+                            int32_t interleaved, float eps, aut_stream_t stream);
+
+/* No passage: a library operator.  Attention to an encoder's states of another
+ * length: request r's queries, rows [cu_q[r], cu_q[r + 1]) of q, attend to the
+ * keys and values of rows [cu_k[r], cu_k[r + 1]), head h of q to key head
+ * h / (heads_q / heads_kv): softmax(scale q k^T) v over the request's keys whose
+ * key_mask byte is not 0 (key_mask NULL: all of them).  Not causal.  A query
+ * without any such key gets zeros.  Masked rows of k and v may hold anything
+ * (infinities, NaN); they do not reach the result.
+ * q, out: device [cu_q[n_seq], heads_q * head_dim] with row strides ld_q, ld_out;
+ * k, v: device [cu_k[n_seq], heads_kv * head_dim] with row strides ld_k, ld_v
+ * (one projection's halves, say); all `dtype` AUT_BF16 or AUT_F16, rows 16-byte
+ * aligned; out must not overlap the inputs, and its rows past cu_q[n_seq] and
+ * columns past the heads stay as they are.  cu_q, cu_k: HOST int32 [n_seq + 1],
+ * non-decreasing from 0.  key_mask: device uint8 [cu_k[n_seq]].  heads_q a
+ * multiple of heads_kv; head_dim 16, 32, 64 or 128; scale > 0.
+ * Scores, the softmax and the sums are fp32; the probabilities enter the P V
+ * product in `dtype`.  workspace: device, 256-byte aligned, at least
+ * aut_cross_attention_workspace_bytes(...) for the same arguments; its contents
+ * need no preparation, and calls that overlap on the GPU need one each.
+ * status and timeout_ms as for aut_linear (a device word for pipeline waits
+ * that ran out of time, may be NULL). */
+aut_status aut_cross_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                               const void *v, int64_t ld_v, void *out, int64_t ld_out,
+                               int32_t dtype, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+                               const int32_t *cu_q, const int32_t *cu_k, int32_t n_seq,
+                               const uint8_t *key_mask, float scale, void *workspace,
+                               size_t ws_bytes, int32_t *status, int32_t timeout_ms,
+                               aut_stream_t stream);
+
+/* No passage: a library helper.  Bytes of device workspace aut_cross_attention
+ * needs for this batch (0 for arguments it refuses). */
+size_t aut_cross_attention_workspace_bytes(int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+                                           const int32_t *cu_q, const int32_t *cu_k,
+                                           int32_t n_seq);
+
 /* No passage: a library helper.  Reads and clears the device status word of a
  * workspace used by aut_window_attention or by aut_encode /
  * aut_frontend / aut_encode_packed (synchronous: call after the stream is
