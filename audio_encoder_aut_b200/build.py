@@ -27,7 +27,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 SOURCES = ["aut_plan.cpp", "aut_kernels.cu", "aut_gemm.cu", "aut_attention.cu", "aut_api.cu",
            "aut_noalloc.cu", "aut_logmel.cu", "aut_inject.cu", "aut_conv1.cu", "aut_int8.cu",
-           "aut_headnorm.cu", "aut_cross.cu"]
+           "aut_headnorm.cu", "aut_cross.cu", "aut_cross_tc.cu"]
 
 
 def nvcc() -> str:

@@ -1,5 +1,6 @@
 // Cross attention over an encoder's packed states: the host plan, the kernel for
-// a few query rows, the join of split requests, and the entry point.
+// a few query rows, the join of split requests, and the entry point.  (Many rows
+// of head_dim 64 and 128 run on the tcgen05 kernel, aut_cross_tc.cu.)
 //
 //   out[i, h] = sum_j p_ij v[j, h'] / sum_j p_ij,   p_ij = 2^(s_ij - max_j s_ij),
 //   s_ij = (q[i, h] . k[j, h']) scale log2(e),   h' = h / group
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     if (item >= a.items) return;
     while (seqs[seq + 1].item <= item) ++seq;
     const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
-    const int nq = nx.q0 - s.q0, splits = (nx.k0 - s.k0 + a.chunk - 1) / a.chunk;
+    const int nq = nx.q0 - s.q0, splits = (nx.part - s.part) / (nq * a.heads_q);
     const int r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
     const size_t step = (size_t)nq * a.heads_q, row0 = (size_t)s.part + r;
     float mx = -INFINITY;
@@ -362,16 +363,25 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 
 // -------------------------------------------------------------------- plan --
 
-// Blocks the splits aim for, and the fewest keys worth a split of their own.
+// The kernels a request may run on, and the join after them.
+enum { kRowsKernel = 0, kTilesKernel = 1, kJoin = 2, kLists = 3 };
+
+// Blocks the splits of one kernel aim for (two a SM), and the fewest keys worth
+// a split of their own.
 constexpr int kTargetItems = 2 * 148;
-constexpr int kMinChunk = 512;
+constexpr int kMinChunk[2] = {512, 512};
 
 struct CrossPlan {
-    int64_t items = 0;      // row-kernel items
-    int64_t join_rows = 0;  // rows of split requests
-    int64_t part_rows = 0;  // partial rows
-    int chunk = kMinChunk;
+    int64_t items[kLists] = {0, 0, 0};  // of each kernel; of the join: rows of split requests
+    int64_t part_rows = 0;              // partial rows
+    int chunk[2] = {0, 0};              // keys of a split
 };
+
+// A request runs on the tcgen05 kernel once its rows pass one 16-row block:
+// from there on the row kernel would read the keys once per block.
+int kernel_of(int64_t nq, int group, int hd) {
+    return hd >= 64 && nq * group > kRows ? kTilesKernel : kRowsKernel;
+}
 
 bool head_dim_ok(int hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
 
@@ -389,53 +399,66 @@ aut_status check_shape(int heads_q, int heads_kv, int hd, const int32_t *cu_q, c
     return AUT_OK;
 }
 
-int64_t row_tiles(int64_t nq, int group) { return (nq * group + kRows - 1) / kRows; }
+// Items of one split of a request.
+int64_t split_items(int kernel, int64_t nq, int group, int heads_kv) {
+    const int rows = kernel == kTilesKernel ? kCrossTileRows : kRows;
+    return (nq * group + rows - 1) / rows * heads_kv;
+}
 
-aut_status plan_cross(int heads_q, int heads_kv, const int32_t *cu_q, const int32_t *cu_k,
+aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
                       int n_seq, CrossPlan *p) {
     const int group = heads_q / heads_kv;
-    int64_t work = 0;  // keys read by all items, unsplit
-    for (int i = 0; i < n_seq; ++i)
-        work += row_tiles(cu_q[i + 1] - cu_q[i], group) * heads_kv * (cu_k[i + 1] - cu_k[i]);
-    // Every split about as long as the GPU's share of the whole.
-    const int64_t share = (work + kTargetItems - 1) / kTargetItems;
-    p->chunk = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk), 1 << 30);
-    p->chunk = (p->chunk + kKeys - 1) / kKeys * kKeys;
+    int64_t work[2] = {0, 0};  // keys read by all of a kernel's items, unsplit
+    for (int i = 0; i < n_seq; ++i) {
+        const int64_t nq = cu_q[i + 1] - cu_q[i];
+        const int kernel = kernel_of(nq, group, hd);
+        work[kernel] += split_items(kernel, nq, group, heads_kv) * (cu_k[i + 1] - cu_k[i]);
+    }
+    // Every split about as long as one block's share of the whole.
+    for (int kernel = 0; kernel < 2; ++kernel) {
+        const int64_t share = (work[kernel] + kTargetItems - 1) / kTargetItems;
+        p->chunk[kernel] = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk[kernel]), 1 << 30);
+        p->chunk[kernel] = (p->chunk[kernel] + 127) / 128 * 128;
+    }
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
-        const int64_t splits = std::max<int64_t>(1, (nk + p->chunk - 1) / p->chunk);
-        p->items += row_tiles(nq, group) * heads_kv * splits;
+        const int kernel = kernel_of(nq, group, hd), chunk = p->chunk[kernel];
+        const int64_t splits = std::max<int64_t>(1, (nk + chunk - 1) / chunk);
+        p->items[kernel] += split_items(kernel, nq, group, heads_kv) * splits;
         if (splits > 1) {
-            p->join_rows += nq * heads_q;
+            p->items[kJoin] += nq * heads_q;
             p->part_rows += nq * heads_q * splits;
         }
     }
-    if (p->items > 0x7fffffffll || p->join_rows > 0x7fffffffll || p->part_rows > 0x7fffffffll)
-        return AUT_ERR_UNSUPPORTED;
+    if (p->part_rows > 0x7fffffffll) return AUT_ERR_UNSUPPORTED;
+    for (int64_t n : p->items)
+        if (n > 0x7fffffffll) return AUT_ERR_UNSUPPORTED;
     return AUT_OK;
 }
 
-// The requests as the row kernel (join = false) or the join sees them.
-void fill_seqs(CrossSeq *out, bool join, const CrossPlan &p, int heads_q, int heads_kv,
+// The requests as kernel `list` (or the join) sees them.
+void fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int heads_kv, int hd,
                const int32_t *cu_q, const int32_t *cu_k, int n_seq) {
+    const int group = heads_q / heads_kv;
     int64_t item = 0, part = 0;
     for (int i = 0; i <= n_seq; ++i) {
         out[i] = {cu_q[i], cu_k[i], (int)item, (int)part};
         if (i == n_seq) break;
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
-        const int64_t splits = std::max<int64_t>(1, (nk + p.chunk - 1) / p.chunk);
-        if (!join)
-            item += row_tiles(nq, heads_q / heads_kv) * heads_kv * splits;
-        else if (splits > 1)
+        const int kernel = kernel_of(nq, group, hd), chunk = p.chunk[kernel];
+        const int64_t splits = std::max<int64_t>(1, (nk + chunk - 1) / chunk);
+        if (list == kernel)
+            item += split_items(kernel, nq, group, heads_kv) * splits;
+        else if (list == kJoin && splits > 1)
             item += nq * heads_q;
         if (splits > 1) part += nq * heads_q * splits;
     }
 }
 
 struct CrossLayout {
-    size_t rows, join, part_o, part_ml, total;
+    size_t list[kLists], part_o, part_ml, total;
 };
 CrossLayout cross_layout(const CrossPlan &p, int hd, int n_seq) {
     CrossLayout l{};
@@ -446,8 +469,7 @@ CrossLayout cross_layout(const CrossPlan &p, int hd, int n_seq) {
         return o;
     };
     const size_t list = n_seq > kCrossInline ? (size_t)(n_seq + 1) * sizeof(CrossSeq) : 0;
-    l.rows = take(list);
-    l.join = take(list);
+    for (size_t &at : l.list) at = take(list);
     l.part_o = take((size_t)p.part_rows * hd * 4);
     l.part_ml = take((size_t)p.part_rows * 8);
     l.total = std::max<size_t>(off, 256);
@@ -489,7 +511,7 @@ extern "C" size_t aut_cross_attention_workspace_bytes(int32_t heads_q, int32_t h
                                                       const int32_t *cu_k, int32_t n_seq) {
     CrossPlan p;
     if (check_shape(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq) != AUT_OK ||
-        plan_cross(heads_q, heads_kv, cu_q, cu_k, n_seq, &p) != AUT_OK)
+        plan_cross(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq, &p) != AUT_OK)
         return 0;
     return cross_layout(p, head_dim, n_seq).total;
 }
@@ -517,7 +539,7 @@ extern "C" aut_status aut_cross_attention(
         return AUT_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(status) & 3u) return AUT_ERR_INVALID_ARG;
     CrossPlan p;
-    st = plan_cross(heads_q, heads_kv, cu_q, cu_k, n_seq, &p);
+    st = plan_cross(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq, &p);
     if (st != AUT_OK) return st;
     const CrossLayout lay = cross_layout(p, head_dim, n_seq);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return AUT_ERR_INVALID_ARG;
@@ -539,7 +561,8 @@ extern "C" aut_status aut_cross_attention(
     a.heads_kv = heads_kv;
     a.group = heads_q / heads_kv;
     a.scale_log2e = (float)((double)scale * 1.4426950408889634);
-    a.chunk = p.chunk;
+    a.status = reinterpret_cast<int *>(status);
+    a.timeout_ns = timeout_ms ? (unsigned long long)timeout_ms * 1000000ull : 4000ull * 1000000ull;
     a.n_seq = n_seq;
     a.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + lay.part_ml);
@@ -547,21 +570,28 @@ extern "C" aut_status aut_cross_attention(
     CrossSeq *list = listed ? new (std::nothrow) CrossSeq[n_seq + 1] : a.inline_seqs;
     if (!list) return AUT_ERR_WORKSPACE;
     aut_status result = AUT_OK;
-    for (int join = 0; join < (p.join_rows > 0 ? 2 : 1) && result == AUT_OK; ++join) {
-        a.items = (int)(join ? p.join_rows : p.items);
-        fill_seqs(list, join != 0, p, heads_q, heads_kv, cu_q, cu_k, n_seq);
+    for (int i = 0; i < kLists && result == AUT_OK; ++i) {
+        if (p.items[i] == 0) continue;
+        a.items = (int)p.items[i];
+        a.chunk = i == kJoin ? 0 : p.chunk[i];
+        fill_seqs(list, i, p, heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
         a.seqs = nullptr;
         if (listed) {
-            CrossSeq *dev = reinterpret_cast<CrossSeq *>(ws + (join ? lay.join : lay.rows));
+            CrossSeq *dev = reinterpret_cast<CrossSeq *>(ws + lay.list[i]);
             a.seqs = dev;
             if (launch_upload(reinterpret_cast<const int32_t *>(list), (size_t)(n_seq + 1) * 4,
                               reinterpret_cast<int32_t *>(dev), s) != cudaSuccess)
                 result = AUT_ERR_CUDA;
         }
-        if (result == AUT_OK &&
-            (dtype == AUT_BF16 ? launch_kernel<__nv_bfloat16>(join != 0, head_dim, a, s)
-                               : launch_kernel<__half>(join != 0, head_dim, a, s)) != cudaSuccess)
-            result = AUT_ERR_CUDA;
+        if (result != AUT_OK) break;
+        cudaError_t e;
+        if (i == kTilesKernel)
+            e = launch_cross_tiles(a, head_dim, dtype == AUT_F16, (int)tk, s);
+        else if (dtype == AUT_BF16)
+            e = launch_kernel<__nv_bfloat16>(i == kJoin, head_dim, a, s);
+        else
+            e = launch_kernel<__half>(i == kJoin, head_dim, a, s);
+        if (e != cudaSuccess) result = AUT_ERR_CUDA;
     }
     if (listed) delete[] list;
     return result;

@@ -1,6 +1,7 @@
 // Cross attention: what its host plan hands to its kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -12,9 +13,9 @@ namespace aut {
 constexpr int kCrossInline = 512;
 
 // One request as one kernel sees it; entry n closes the list.  Its work items
-// are item .. next item: [split][key head][row tile].  With more than one
-// split its partial results start at row `part` of the partial buffer:
-// [split][query][query head].
+// are item .. next item (none, if another kernel handles it): [split][key
+// head][row tile].  With more than one split its partial results are rows
+// part .. next part of the partial buffer: [split][query][query head].
 struct CrossSeq {
     int q0, k0, item, part;
 };
@@ -30,6 +31,8 @@ struct CrossArgs {
     int n_seq, items;
     float *part_o;    // [partial rows][head_dim], fp32, over each split's own row maximum
     float2 *part_ml;  // that maximum (times scale_log2e) and the sum of 2^(s - max)
+    int *status;
+    unsigned long long timeout_ns;
     const CrossSeq *seqs;  // in the workspace; null: `inline_seqs`
     CrossSeq inline_seqs[kCrossInline + 1];
 };
@@ -48,5 +51,12 @@ __device__ __forceinline__ int cross_find(const CrossSeq *seqs, int n_seq, int i
     }
     return lo;
 }
+
+// The tcgen05 kernel (aut_cross_tc.cu), for head_dim 64 and 128: tiles of
+// kCrossTileRows rows (query, head of the group) and 128 keys.
+constexpr int kCrossTileRows = 128;
+constexpr int kCrossTileKeys = 128;
+// tk: rows of k and v.  f16: the element type (bf16 otherwise).
+cudaError_t launch_cross_tiles(const CrossArgs &a, int head_dim, bool f16, int tk, cudaStream_t st);
 
 }  // namespace aut

@@ -223,6 +223,18 @@ AUT_DEV void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint
         : "memory");
 }
 
+// The same with A in tensor memory: its row r in lane r, two 16-bit elements of
+// K to a 32-bit column.
+AUT_DEV void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // D(tmem) (+)= A(smem) * B(smem)^T, signed 8-bit inputs, int32 accumulate.
 AUT_DEV void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                        uint32_t accumulate) {
@@ -287,6 +299,21 @@ AUT_DEV void tmem_st16(uint32_t taddr, const float (&v)[16]) {
         : "memory");
 }
 
+// Stores 32 consecutive 32-bit columns into this thread's TMEM lane.
+AUT_DEV void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
 // Shared-memory matrix descriptor for a K-major operand tile written by TMA
 // with 128-byte swizzling: rows of 128 bytes (64 bf16 of K), 8-row swizzle
 // atoms 1024 bytes apart.  Fields: start address >> 4 (bits 0-13), leading
@@ -308,6 +335,14 @@ AUT_DEV uint64_t smem_desc_sw128_mn(const void *tile) {
     const uint64_t addr = smem_addr(tile);
     return ((addr & 0x3FFFFull) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
            (2ull << 61);
+}
+
+// The same for a tile of several 64-wide N groups, `group_bytes` apart (the
+// leading byte offset, bits 16-29).
+AUT_DEV uint64_t smem_desc_sw128_mn(const void *tile, uint32_t group_bytes) {
+    const uint64_t addr = smem_addr(tile);
+    return ((addr & 0x3FFFFull) >> 4) | ((uint64_t)(group_bytes >> 4) << 16) | (64ull << 32) |
+           (1ull << 46) | (2ull << 61);
 }
 
 // Fence making this thread's generic-proxy shared-memory writes visible to the
