@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     const int tile = item % tiles;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const int splits = max(1, (nk + a.chunk - 1) / a.chunk);
-    const int key0 = s.k0 + split * a.chunk, key1 = min(nx.k0, key0 + a.chunk);
+    const CrossSplits sp = cross_splits(nk, a.chunk);
+    const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
     const int n_blocks = (key1 - key0 + kKeys - 1) / kKeys;  // 0 for a request without keys
 
     // Row r of the tile: query (tile 16 + r) / group, head hk group + (tile 16 + r) % group.
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = fmaf(f, join[(w * kRows + r) * kLd + 8 * c + e], v[e]);
         }
-        if (splits > 1) {
+        if (sp.n > 1) {
             const size_t row = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
             store8(a.part_o + row * HD + 8 * c, v);
             if (c == 0) a.part_ml[row] = make_float2(mx, sum);
@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 // The kernels a request may run on, and the join after them.
 enum { kRowsKernel = 0, kTilesKernel = 1, kJoin = 2, kLists = 3 };
 
-// Blocks the splits of one kernel aim for (two a SM), and the fewest keys worth
-// a split of their own.
-constexpr int kTargetItems = 2 * 148;
+// Blocks the splits of one kernel aim for (two a SM, or one), and the fewest
+// keys worth a split of their own.
+constexpr int kTargetItems[2] = {2 * 148, 148};
 constexpr int kMinChunk[2] = {512, 512};
 
 struct CrossPlan {
@@ -416,15 +416,15 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
     }
     // Every split about as long as one block's share of the whole.
     for (int kernel = 0; kernel < 2; ++kernel) {
-        const int64_t share = (work[kernel] + kTargetItems - 1) / kTargetItems;
+        const int64_t share = (work[kernel] + kTargetItems[kernel] - 1) / kTargetItems[kernel];
         p->chunk[kernel] = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk[kernel]), 1 << 30);
         p->chunk[kernel] = (p->chunk[kernel] + 127) / 128 * 128;
     }
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
-        const int kernel = kernel_of(nq, group, hd), chunk = p->chunk[kernel];
-        const int64_t splits = std::max<int64_t>(1, (nk + chunk - 1) / chunk);
+        const int kernel = kernel_of(nq, group, hd);
+        const int64_t splits = cross_splits((int)nk, p->chunk[kernel]).n;
         p->items[kernel] += split_items(kernel, nq, group, heads_kv) * splits;
         if (splits > 1) {
             p->items[kJoin] += nq * heads_q;
@@ -447,8 +447,8 @@ void fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int hea
         if (i == n_seq) break;
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
-        const int kernel = kernel_of(nq, group, hd), chunk = p.chunk[kernel];
-        const int64_t splits = std::max<int64_t>(1, (nk + chunk - 1) / chunk);
+        const int kernel = kernel_of(nq, group, hd);
+        const int64_t splits = cross_splits((int)nk, p.chunk[kernel]).n;
         if (list == kernel)
             item += split_items(kernel, nq, group, heads_kv) * splits;
         else if (list == kJoin && splits > 1)

@@ -27,7 +27,7 @@ struct CrossArgs {
     long long ld_q, ld_k, ld_v, ld_out;  // elements
     int heads_q, heads_kv, group;
     float scale_log2e;
-    int chunk;        // keys of a split (a request has ceil(keys / chunk) of them, at least one)
+    int chunk;        // most keys of a split
     int n_seq, items;
     float *part_o;    // [partial rows][head_dim], fp32, over each split's own row maximum
     float2 *part_ml;  // that maximum (times scale_log2e) and the sum of 2^(s - max)
@@ -36,6 +36,19 @@ struct CrossArgs {
     const CrossSeq *seqs;  // in the workspace; null: `inline_seqs`
     CrossSeq inline_seqs[kCrossInline + 1];
 };
+
+// A request's splits: as few as `chunk` allows (at least one), as even as whole
+// 128-key tiles allow.
+struct CrossSplits {
+    int n, keys;  // splits, and keys of each but the last
+};
+__host__ __device__ inline CrossSplits cross_splits(int nk, int chunk) {
+    int n = (int)(((long long)nk + chunk - 1) / chunk);
+    if (n <= 1) return {1, nk};
+    const int keys = (int)((((long long)nk + n - 1) / n + 127) / 128 * 128);
+    n = (int)(((long long)nk + keys - 1) / keys);
+    return {n, keys};
+}
 
 // The item's request: the last one that begins at or before `item`.  The whole
 // warp searches, 32 probes a round.
@@ -52,9 +65,9 @@ __device__ __forceinline__ int cross_find(const CrossSeq *seqs, int n_seq, int i
     return lo;
 }
 
-// The tcgen05 kernel (aut_cross_tc.cu), for head_dim 64 and 128: tiles of
-// kCrossTileRows rows (query, head of the group) and 128 keys.
-constexpr int kCrossTileRows = 128;
+// The tcgen05 kernel (aut_cross_tc.cu), for head_dim 64 and 128: kCrossTileRows
+// rows (query, head of the group) a block, keys in tiles of 128.
+constexpr int kCrossTileRows = 256;
 constexpr int kCrossTileKeys = 128;
 // tk: rows of k and v.  f16: the element type (bf16 otherwise).
 cudaError_t launch_cross_tiles(const CrossArgs &a, int head_dim, bool f16, int tk, cudaStream_t st);

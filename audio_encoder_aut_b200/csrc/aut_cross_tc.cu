@@ -7,19 +7,23 @@
 //   then the old maximum serves as the softmax's reference, which cancels in
 //   O / sum, and P stays at most 2^8.
 //
-// Warp roles (192 threads, one tile of rows and one split of keys per block):
-//   warps 0-3  softmax: thread r owns row r (TMEM lane r), so maximum and sum
-//              need no exchange; also Q into shared memory and O out
-//   warp 4     TMA producer: K and V tiles (128 keys, 128-byte swizzle) in
-//              turn through a ring of slots
-//   warp 5     TMEM allocation; one thread issues the products.  P is the A
+// Warp roles (384 threads; two tiles of rows, 256 rows in all, and one split of
+// keys per block):
+//   warps 0-7  softmax, four warps a tile: thread r owns row r (TMEM lane r), so
+//              maximum and sum need no exchange; also Q into shared memory and O
+//              out
+//   warp 8     TMA producer: K and V tiles (128 keys, 128-byte swizzle) in
+//              turn through a ring of slots, each read by both row tiles
+//   warp 9     TMEM allocation; one thread issues the products.  P is the A
 //              operand from tensor memory
-// Two blocks share a SM (256 tensor-memory columns and half the shared memory
-// each): while one runs its softmax, the other's products run, without any
-// exchange between them.  With head_dim 64 the P columns fit beside S, and the
-// next tile's S is computed while this tile's softmax runs; with 128 P takes the
-// place of the S it came from, and the next S follows P V in the tensor pipe's
-// order.
+// The one issuer alternates between the row tiles, so that while one tile's
+// softmax runs the other's products do.  (As two blocks a SM with one tile each,
+// the two issuers' products share the tensor pipe instruction by instruction, and
+// both blocks fall into step: softmax against softmax, products against products,
+// 528 us where the alternating issuer takes @ALT@ for 16 x 512 x 4096, 16 heads of
+// 128.)  With head_dim 64 the P columns fit beside S, and the next tile's S is
+// computed while this tile's softmax runs; with 128 P takes the place of the S
+// it came from, and the next S follows P V in the tensor pipe's order.
 //
 // Keys past the request's end or masked out score -inf, and their V rows are
 // zeroed in shared memory (they may hold anything, and 0 * NaN is NaN).
@@ -37,24 +41,31 @@
 namespace aut {
 namespace {
 
-constexpr int kM = kCrossTileRows, kN = kCrossTileKeys;
-constexpr int kThreads = 192;
-constexpr uint32_t kTmemCols = 256;
+constexpr int kM = 128, kN = kCrossTileKeys;  // rows of a tile, keys of a tile
+constexpr int kSoftmaxWarps = 8;              // four per row tile
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups; two warps idle
+// Registers a thread: 168 at launch (three warps to a quarter of the register
+// file), of which the third warpgroup gives some to the softmax, whose rows of
+// 128 scores otherwise spill.  256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+constexpr uint32_t kTmemCols = 512;
 
 template <int HD>
 struct TcCfg {
-    static constexpr int kTileBytes = kN * HD * 2;    // K or V of a tile; Q as well
+    static constexpr int kTileBytes = kN * HD * 2;    // K or V of a tile; Q of a row tile as well
     static constexpr int kAtom = kN * 128;            // 128 rows of 64 elements
-    static constexpr int kSlots = HD == 64 ? 5 : 2;   // K and V tiles in shared memory
+    static constexpr int kSlots = HD == 64 ? 10 : 5;  // K and V tiles in shared memory
     static constexpr bool kEarlyS = HD == 64;         // the next S before this P V
-    static constexpr uint32_t kColO = kN;             // O behind S
-    static constexpr uint32_t kColP = kEarlyS ? kN + HD : 0;
-    static constexpr int kOffBar = kTileBytes * (1 + kSlots);
-    // full, empty [kSlots]; q_full, s_full, s_read, p_full, pv_done, mma_done
-    static constexpr int kBars = 2 * kSlots + 6;
+    // Tensor memory: S of the row tiles, then their O; P beside them or over S.
+    static constexpr uint32_t kColO = 2 * kN;
+    static constexpr uint32_t kColP = kEarlyS ? kColO + 2 * HD : 0;
+    static constexpr uint32_t kStepP = kEarlyS ? kN / 2 : kN;  // from one row tile's P to the other's
+    static constexpr int kOffBar = kTileBytes * (2 + kSlots);
+    // full, empty [kSlots]; q_full; s_full, s_read, p_full, pv_done [2]; mma_done
+    static constexpr int kBars = 2 * kSlots + 10;
     static constexpr int kSmem = 1024 + kOffBar + kBars * 8 + 16;
-    static_assert(kColO + HD + (kEarlyS ? kN / 2 : 0) <= kTmemCols, "tensor memory");
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks a SM");
+    static_assert(kColO + 2 * HD + (kEarlyS ? kN : 0) <= kTmemCols, "tensor memory");
+    static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 template <typename T>
@@ -68,7 +79,7 @@ constexpr uint32_t idesc_pv() {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     cross_tiles_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CrossArgs a) {
@@ -77,15 +88,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *slots = sm + Cfg::kTileBytes;  // Q first
+    uint8_t *slots = sm + 2 * Cfg::kTileBytes;  // behind the row tiles' Q
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Cfg::kOffBar);
     uint64_t *empty = full + kSlots;
     uint64_t *q_full = empty + kSlots;
-    uint64_t *s_full = q_full + 1;
-    uint64_t *s_read = s_full + 1;
-    uint64_t *p_full = s_read + 1;
-    uint64_t *pv_done = p_full + 1;
-    uint64_t *mma_done = pv_done + 1;
+    uint64_t *s_full = q_full + 1;    // [2] per row tile, as the next three
+    uint64_t *s_read = s_full + 2;
+    uint64_t *p_full = s_read + 2;
+    uint64_t *pv_done = p_full + 2;
+    uint64_t *mma_done = pv_done + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 1);
     int *abort_flag = reinterpret_cast<int *>(tslot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,11 +112,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        mbar_init(q_full, 4);
-        mbar_init(s_full, 1);
-        mbar_init(s_read, 4);
-        mbar_init(p_full, 4);
-        mbar_init(pv_done, 1);
+        mbar_init(q_full, kSoftmaxWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(s_read + i, 4);
+            mbar_init(p_full + i, 4);
+            mbar_init(pv_done + i, 1);
+        }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -113,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_prefetch_desc(&tm_v);
     }
     pdl_wait();  // before the tensor memory: the previous kernel's blocks have all left
-    if (warp == 5) {
+    if (warp == kSoftmaxWarps + 1) {
         tmem_alloc(tslot, kTmemCols);
         tmem_relinquish();
     }
@@ -127,17 +140,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
     const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
     const int nq = nx.q0 - s.q0, nk = nx.k0 - s.k0;
-    const int rows = nq * a.group, tiles = (rows + kM - 1) / kM;
+    const int rows = nq * a.group, tiles = (rows + kCrossTileRows - 1) / kCrossTileRows;
     int item = (int)blockIdx.x - s.item;
-    const int tile = item % tiles;
+    const int row0 = item % tiles * kCrossTileRows;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const int splits = max(1, (nk + a.chunk - 1) / a.chunk);
-    const int key0 = s.k0 + split * a.chunk, key1 = min(nx.k0, key0 + a.chunk);
+    const CrossSplits sp = cross_splits(nk, a.chunk);
+    const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
     const int n = (key1 - key0 + kN - 1) / kN;  // key tiles; 0 for a request without keys
+    const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
 
-    if (warp == 4) {
-        if (lane == 0) {
+    if (warp >= kSoftmaxWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kSoftmaxWarps && lane == 0) {
             // ------------------------------------------------ TMA producer --
             // Copy t: K (t even) or V (t odd) of key tile t / 2, in slot t % kSlots.
             bool ok = true;
@@ -163,74 +178,100 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mbar_wait(full + u % kSlots, (uint32_t)(u / kSlots) & 1u, nullptr, lim - used);
             }
         }
-    } else if (warp == 5) {
-        if (lane == 0) {
+        if (warp == kSoftmaxWarps + 1 && lane == 0) {
             // -------------------------------------------------- MMA issuer --
             auto n16 = [&](int j) { return min(kN, (key1 - key0 - j * kN + 15) & ~15); };
-            auto issue_s = [&](int j) -> bool {
-                const int t = 2 * j, i = t % kSlots;
-                if (!mbar_wait(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim)) return false;
+            // Slots of the next K and V tile and their phases.
+            int ki = 0, vi = 1 % kSlots;
+            uint32_t kp = 0, vp = 0;
+            const uint64_t slot_k = smem_desc_sw128(slots), slot_v = smem_desc_sw128_mn(slots, Cfg::kAtom);
+            const uint64_t q_desc = smem_desc_sw128(sm);
+            constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4, kAtom16 = Cfg::kAtom >> 4;
+            // The wait for a slot belongs to its first user, its release to its last.
+            auto issue_s = [&](int j, int rt) -> bool {
+                if (rt == 0 && !mbar_wait(full + ki, kp, abort_v, lim)) return false;
                 tc_fence_after();
                 const uint32_t id = idesc_qk<T>(n16(j));
+                const uint64_t qd = q_desc + rt * kTile16, kd = slot_k + ki * kTile16;
 #pragma unroll
-                for (int c = 0; c < HD / 16; ++c) {
-                    const int at = (c >> 2) * Cfg::kAtom;
-                    tc_mma_bf16(tmem, smem_desc_sw128(sm + at) + 2 * (c & 3),
-                                smem_desc_sw128(slots + i * Cfg::kTileBytes + at) + 2 * (c & 3), id,
-                                c > 0);
+                for (int c = 0; c < HD / 16; ++c)
+                    tc_mma_bf16(tmem + rt * kN, qd + (c >> 2) * kAtom16 + 2 * (c & 3),
+                                kd + (c >> 2) * kAtom16 + 2 * (c & 3), id, c > 0);
+                tc_commit(s_full + rt);
+                if (rt == n_rt - 1) {
+                    tc_commit(empty + ki);
+                    if ((ki += 2) >= kSlots) {
+                        ki -= kSlots;
+                        kp ^= 1u;
+                    }
                 }
-                tc_commit(s_full);
-                tc_commit(empty + i);
+                return true;
+            };
+            auto issue_pv = [&](int j, int rt) -> bool {
+                if (!mbar_wait(p_full + rt, (uint32_t)j & 1u, abort_v, lim) ||
+                    (rt == 0 && !mbar_wait(full + vi, vp, abort_v, lim)))
+                    return false;
+                tc_fence_after();
+                const int steps = n16(j) / 16;
+                const uint64_t vd = slot_v + vi * kTile16;
+                const uint32_t d = tmem + Cfg::kColO + rt * HD, p = tmem + Cfg::kColP + rt * Cfg::kStepP;
+#pragma unroll
+                for (int c = 0; c < kN / 16; ++c)
+                    if (c < steps)
+                        tc_mma_f16_ts(d, p + 8 * c, vd + c * (16 * 128 / 16), idesc_pv<T, HD>(),
+                                      (j | c) > 0);
+                tc_commit(pv_done + rt);
+                if (rt == n_rt - 1) {
+                    tc_commit(empty + vi);
+                    if ((vi += 2) >= kSlots) {
+                        vi -= kSlots;
+                        vp ^= 1u;
+                    }
+                }
                 return true;
             };
             bool ok = n == 0 || mbar_wait(q_full, 0, abort_v, lim);
-            if (ok && n > 0) ok = issue_s(0);
-            for (int j = 0; ok && j < n; ++j) {
-                if (Cfg::kEarlyS && j + 1 < n) {
-                    ok = mbar_wait(s_read, (uint32_t)j & 1u, abort_v, lim);
-                    if (ok) tc_fence_after();
-                    ok = ok && issue_s(j + 1);
+            if (n > 0)
+                for (int rt = 0; ok && rt < n_rt; ++rt) ok = issue_s(0, rt);
+            for (int j = 0; ok && j < n; ++j)
+                for (int rt = 0; ok && rt < n_rt; ++rt) {
+                    if (Cfg::kEarlyS && j + 1 < n)
+                        ok = mbar_wait(s_read + rt, (uint32_t)j & 1u, abort_v, lim) && issue_s(j + 1, rt);
+                    ok = ok && issue_pv(j, rt);
+                    if (!Cfg::kEarlyS && j + 1 < n) ok = ok && issue_s(j + 1, rt);
                 }
-                const int t = 2 * j + 1, i = t % kSlots;
-                ok = ok && mbar_wait(p_full, (uint32_t)j & 1u, abort_v, lim) &&
-                     mbar_wait(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim);
-                if (!ok) break;
-                tc_fence_after();
-                const int steps = n16(j) / 16;
-                for (int c = 0; c < steps; ++c)
-                    tc_mma_f16_ts(tmem + Cfg::kColO, tmem + Cfg::kColP + 8 * c,
-                                  smem_desc_sw128_mn(slots + i * Cfg::kTileBytes + c * 16 * 128,
-                                                     Cfg::kAtom),
-                                  idesc_pv<T, HD>(), j > 0 || c > 0);
-                tc_commit(pv_done);
-                tc_commit(empty + i);
-                if (!Cfg::kEarlyS && j + 1 < n) ok = issue_s(j + 1);
-            }
             if (!ok) signal_abort();
             // Every product this thread issued has completed before TMEM is released.
             tc_commit(mma_done);
             mbar_wait(mma_done, 0, nullptr, lim);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------- softmax --
-        // Q: 16 bytes a thread, rows of the tile one after the other.
+        // Q: 16 bytes a thread, rows one after the other.
         constexpr int kChunks = HD / 8;
-        for (int i = threadIdx.x; i < kM * kChunks; i += 128) {
-            const int r = i / kChunks, c = i % kChunks, at = tile * kM + r;
-            const int tok = at / a.group, head = hk * a.group + at - tok * a.group;
+        for (int i = threadIdx.x; i < n_rt * kM * kChunks; i += 32 * kSoftmaxWarps) {
+            const int r = i / kChunks, c = i % kChunks, at = row0 + r;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (at < rows)
+            if (at < rows) {
+                const int tok = at / a.group, head = hk * a.group + at - tok * a.group;
                 v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
                                                      (size_t)(s.q0 + tok) * a.ld_q + head * HD + c * 8);
-            *reinterpret_cast<uint4 *>(sm + (c >> 3) * Cfg::kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+            }
+            *reinterpret_cast<uint4 *>(sm + (r >> 7) * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
+                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
 
-        const int row = warp * 32 + lane;
-        const bool active = tile * kM + warp * 32 < rows;  // some row of the warp exists
-        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+        const int rt = warp >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;  // of the row tile, and TMEM lane
+        const bool used = rt < n_rt;
+        const bool active = row0 + rt * kM + quad * 32 < rows;  // some row of the warp exists
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t t_s = trow + rt * kN, t_o = trow + Cfg::kColO + rt * HD,
+                       t_p = trow + Cfg::kColP + rt * Cfg::kStepP;
         const float2 scale2 = make_float2(a.scale_log2e, a.scale_log2e);
         float m = -INFINITY, l = 0.f;  // the softmax's reference (unscaled) and the row's sum
         bool ok = true;
@@ -245,11 +286,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         uint32_t next[4];
         tile_keys(0, next);
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; used && j < n; ++j) {
             const uint32_t keys[4] = {next[0], next[1], next[2], next[3]};
             const bool whole = (keys[0] & keys[1] & keys[2] & keys[3]) == 0xffffffffu;
             tile_keys(j + 1, next);
-            if (!mbar_wait_warp(s_full, (uint32_t)j & 1u, abort_v, lim)) {
+            if (!mbar_wait_warp(s_full + rt, (uint32_t)j & 1u, abort_v, lim)) {
                 ok = false;
                 break;
             }
@@ -257,17 +298,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             float v[4][32];
             if (active) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(trow + 32 * c, v[c]);
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, v[c]);
                 tc_wait_ld();
             }
             if (Cfg::kEarlyS) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s_read);
+                if (lane == 0) mbar_arrive(s_read + rt);
             }
-            float neg = 0.f;  // -(reference) in units of the exponent
+            float neg = 0.f, f = 1.f;  // -(reference) in units of the exponent; O's factor
             bool shrink = false;
-            float f = 1.f;
             if (active) {
                 if (!whole) {
 #pragma unroll
@@ -293,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // P into tensor memory (over S, or over the last P) and O scaled only
             // once the previous P V is done.
-            if (j > 0 && !mbar_wait_warp(pv_done, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
+            if (j > 0 && !mbar_wait_warp(pv_done + rt, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
             if (active) {
+                tc_fence_after();
                 const float2 neg2 = make_float2(neg, neg);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -312,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
                         p[e >> 1] = pack2<T>(q.x, q.y);
                     }
-                    tmem_st32(trow + Cfg::kColP + 32 * h, p);
+                    tmem_st32(t_p + 32 * h, p);
                 }
                 const float2 all = fadd2(sum[0], sum[1]);
                 l += all.x + all.y;
@@ -320,22 +360,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 16) {
                         float o[16];
-                        tmem_ld16(trow + Cfg::kColO + c, o);
+                        tmem_ld16(t_o + c, o);
                         tc_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] *= f;
-                        tmem_st16(trow + Cfg::kColO + c, o);
+                        tmem_st16(t_o + c, o);
                     }
                 }
                 tc_wait_st();
             }
-            if (!whole) {  // this thread's key's V row, if it is not read
+            // This thread's key's V row, if it is not read.  The first row tile's
+            // P V, which waits for this, comes before the second's.
+            if (!whole && rt == 0) {
                 const int t = 2 * j + 1, i = t % kSlots;
                 if (!mbar_wait_warp(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim)) {
                     ok = false;
                     break;
                 }
-                if (!((keys[warp] >> lane) & 1u))
+                if (!((keys[quad] >> lane) & 1u))
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
                         *reinterpret_cast<uint4 *>(slots + i * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
@@ -344,22 +386,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) mbar_arrive(p_full + rt);
         }
-        if (ok && n > 0) ok = mbar_wait_warp(pv_done, (uint32_t)(n - 1) & 1u, abort_v, lim);
+        if (ok && used && n > 0) ok = mbar_wait_warp(pv_done + rt, (uint32_t)(n - 1) & 1u, abort_v, lim);
         if (!ok && lane == 0) signal_abort();
         if (ok && active) {
             tc_fence_after();
-            const int at = tile * kM + row, tok = at / a.group, head = hk * a.group + at - tok * a.group;
+            const int at = row0 + rt * kM + row, tok = at / a.group, head = hk * a.group + at - tok * a.group;
             const bool in = at < rows;
-            const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+            const float inv = sp.n > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // no key: zeros
             const size_t prow = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
             T *dst = static_cast<T *>(a.out) + (size_t)(s.q0 + tok) * a.ld_out + head * HD;
 #pragma unroll
             for (int c = 0; c < HD; c += 32) {
                 float o[32];
                 if (n > 0) {
-                    tmem_ld32(trow + Cfg::kColO + c, o);
+                    tmem_ld32(t_o + c, o);
                     tc_wait_ld();
                 }
                 if (in) {
@@ -368,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         float w[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = n > 0 ? o[e + i] * inv : 0.f;
-                        if (splits > 1)
+                        if (sp.n > 1)
                             store8(a.part_o + prow * HD + c + e, w);
                         else
                             store8(dst + c + e, w);
@@ -376,13 +418,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 __syncwarp();  // converged again before the next warp-wide load
             }
-            if (in && splits > 1) a.part_ml[prow] = make_float2(m * a.scale_log2e, l);
+            if (in && sp.n > 1) a.part_ml[prow] = make_float2(m * a.scale_log2e, l);
         }
     }
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kSoftmaxWarps + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
