@@ -78,6 +78,16 @@ constexpr uint32_t idesc_pv() {
     return idesc_qk<T>(HD) | (1u << 16);
 }
 
+// Maximum of a row's 128 scores, in four chains.
+AUT_DEV float row_max(const float (&v)[4][32]) {
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) top[c] = fmax3(top[c], v[c][e], v[c][e + 1]);
+    return fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_tiles_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -306,9 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read + rt);
             }
-            float neg = 0.f, f = 1.f;  // -(reference) in units of the exponent; O's factor
-            bool shrink = false;
+            // P into tensor memory (over S, or over the last P) and O scaled only
+            // once the previous P V is done; with P over S, this S came after it.
+            if (Cfg::kEarlyS && j > 0 && !mbar_wait_warp(pv_done + rt, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
+                ok = false;
+                break;
+            }
             if (active) {
+                tc_fence_after();
                 if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -316,47 +331,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             v[c][e] = keys[c] & (1u << e) ? v[c][e] : -INFINITY;
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (j == 0) m = row_max(v);
+                // P by the reference so far, the maximum beside it; once more by
+                // the new one in the rare case that it has grown too much.
+                float f = 1.f, sum;
+                while (true) {
+                    const float neg = m == -INFINITY ? 0.f : -m * a.scale_log2e;
+                    const float2 neg2 = make_float2(neg, neg);
+                    float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) top[c] = fmax3(top[c], v[c][e], v[c][e + 1]);
-                const float mn = fmaxf(m, fmaxf(fmax3(top[0], top[1], top[2]), top[3]));
-                const bool grown = (mn - m) * a.scale_log2e > 8.f;  // also from no key at all
-                shrink = __any_sync(0xffffffffu, grown);
-                if (grown) {
-                    f = ex2_approx((m - mn) * a.scale_log2e);
-                    m = mn;
-                    l *= f;
-                }
-                neg = m == -INFINITY ? 0.f : -m * a.scale_log2e;
-            }
-            // P into tensor memory (over S, or over the last P) and O scaled only
-            // once the previous P V is done.
-            if (j > 0 && !mbar_wait_warp(pv_done + rt, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
-                ok = false;
-                break;
-            }
-            if (active) {
-                tc_fence_after();
-                const float2 neg2 = make_float2(neg, neg);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float *x = &v[2 * h + (e >> 5)][e & 31];
-                        const float2 y = ffma2(make_float2(x[0], x[1]), scale2, neg2);
-                        const float2 q = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
-                        p[e >> 1] = pack2<T>(q.x, q.y);
+                        for (int e = 0; e < 64; e += 2) {
+                            const float *x = &v[2 * h + (e >> 5)][e & 31];
+                            top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], x[0], x[1]);
+                            const float2 y = ffma2(make_float2(x[0], x[1]), scale2, neg2);
+                            const float2 q = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            s2[(e >> 1) & 1] = fadd2(s2[(e >> 1) & 1], q);
+                            p[e >> 1] = pack2<T>(q.x, q.y);
+                        }
+                        tmem_st32(t_p + 32 * h, p);
                     }
-                    tmem_st32(t_p + 32 * h, p);
+                    const float2 all = fadd2(s2[0], s2[1]);
+                    sum = all.x + all.y;
+                    const float mn = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+                    const bool grown = (mn - m) * a.scale_log2e > 8.f;  // also from no key at all
+                    if (!__any_sync(0xffffffffu, grown)) break;
+                    if (grown) {
+                        f *= ex2_approx((m - mn) * a.scale_log2e);
+                        m = mn;
+                    }
                 }
-                const float2 all = fadd2(sum[0], sum[1]);
-                l += all.x + all.y;
-                if (shrink && j > 0) {
+                l = l * f + sum;
+                if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 16) {
                         float o[16];
