@@ -188,8 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait(full + u % kSlots, (uint32_t)(u / kSlots) & 1u, nullptr, lim - used);
             }
         }
-        if (warp == kSoftmaxWarps + 1 && lane == 0) {
+        if (warp == kSoftmaxWarps + 1) {
             // -------------------------------------------------- MMA issuer --
+            // The whole warp runs the loop, so that descriptors are warp-uniform
+            // values (kept in uniform registers, which the products take); one
+            // lane issues.
+            const bool leader = elect_one();
             auto n16 = [&](int j) { return min(kN, (key1 - key0 - j * kN + 15) & ~15); };
             // Slots of the next K and V tile and their phases.
             int ki = 0, vi = 1 % kSlots;
@@ -199,17 +203,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4, kAtom16 = Cfg::kAtom >> 4;
             // The wait for a slot belongs to its first user, its release to its last.
             auto issue_s = [&](int j, int rt) -> bool {
-                if (rt == 0 && !mbar_wait(full + ki, kp, abort_v, lim)) return false;
+                if (rt == 0 && !mbar_wait_warp(full + ki, kp, abort_v, lim)) return false;
                 tc_fence_after();
                 const uint32_t id = idesc_qk<T>(n16(j));
                 const uint64_t qd = q_desc + rt * kTile16, kd = slot_k + ki * kTile16;
+                if (leader) {
 #pragma unroll
-                for (int c = 0; c < HD / 16; ++c)
-                    tc_mma_bf16(tmem + rt * kN, qd + (c >> 2) * kAtom16 + 2 * (c & 3),
-                                kd + (c >> 2) * kAtom16 + 2 * (c & 3), id, c > 0);
-                tc_commit(s_full + rt);
+                    for (int c = 0; c < HD / 16; ++c)
+                        tc_mma_bf16(tmem + rt * kN, qd + (c >> 2) * kAtom16 + 2 * (c & 3),
+                                    kd + (c >> 2) * kAtom16 + 2 * (c & 3), id, c > 0);
+                    tc_commit(s_full + rt);
+                    if (rt == n_rt - 1) tc_commit(empty + ki);
+                }
+                __syncwarp();
                 if (rt == n_rt - 1) {
-                    tc_commit(empty + ki);
                     if ((ki += 2) >= kSlots) {
                         ki -= kSlots;
                         kp ^= 1u;
@@ -218,21 +225,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             auto issue_pv = [&](int j, int rt) -> bool {
-                if (!mbar_wait(p_full + rt, (uint32_t)j & 1u, abort_v, lim) ||
-                    (rt == 0 && !mbar_wait(full + vi, vp, abort_v, lim)))
+                if (!mbar_wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim) ||
+                    (rt == 0 && !mbar_wait_warp(full + vi, vp, abort_v, lim)))
                     return false;
                 tc_fence_after();
                 const int steps = n16(j) / 16;
                 const uint64_t vd = slot_v + vi * kTile16;
                 const uint32_t d = tmem + Cfg::kColO + rt * HD, p = tmem + Cfg::kColP + rt * Cfg::kStepP;
+                if (leader) {
 #pragma unroll
-                for (int c = 0; c < kN / 16; ++c)
-                    if (c < steps)
-                        tc_mma_f16_ts(d, p + 8 * c, vd + c * (16 * 128 / 16), idesc_pv<T, HD>(),
-                                      (j | c) > 0);
-                tc_commit(pv_done + rt);
+                    for (int c = 0; c < kN / 16; ++c)
+                        if (c < steps)
+                            tc_mma_f16_ts(d, p + 8 * c, vd + c * (16 * 128 / 16), idesc_pv<T, HD>(),
+                                          (j | c) > 0);
+                    tc_commit(pv_done + rt);
+                    if (rt == n_rt - 1) tc_commit(empty + vi);
+                }
+                __syncwarp();
                 if (rt == n_rt - 1) {
-                    tc_commit(empty + vi);
                     if ((vi += 2) >= kSlots) {
                         vi -= kSlots;
                         vp ^= 1u;
@@ -240,20 +250,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            bool ok = n == 0 || mbar_wait(q_full, 0, abort_v, lim);
+            bool ok = n == 0 || mbar_wait_warp(q_full, 0, abort_v, lim);
             if (n > 0)
                 for (int rt = 0; ok && rt < n_rt; ++rt) ok = issue_s(0, rt);
             for (int j = 0; ok && j < n; ++j)
                 for (int rt = 0; ok && rt < n_rt; ++rt) {
                     if (Cfg::kEarlyS && j + 1 < n)
-                        ok = mbar_wait(s_read + rt, (uint32_t)j & 1u, abort_v, lim) && issue_s(j + 1, rt);
+                        ok = mbar_wait_warp(s_read + rt, (uint32_t)j & 1u, abort_v, lim) && issue_s(j + 1, rt);
                     ok = ok && issue_pv(j, rt);
                     if (!Cfg::kEarlyS && j + 1 < n) ok = ok && issue_s(j + 1, rt);
                 }
-            if (!ok) signal_abort();
-            // Every product this thread issued has completed before TMEM is released.
-            tc_commit(mma_done);
-            mbar_wait(mma_done, 0, nullptr, lim);
+            // Every product the leader issued has completed before TMEM is released.
+            if (leader) {
+                if (!ok) signal_abort();
+                tc_commit(mma_done);
+                mbar_wait(mma_done, 0, nullptr, lim);
+            }
+            __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));

@@ -203,6 +203,17 @@ AUT_DEV void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 AUT_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 AUT_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// True for one lane of a converged warp.
+AUT_DEV bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
 // Arrives on `bar` once every tcgen05 operation this thread issued before has
 // completed.
 AUT_DEV void tc_commit(uint64_t *bar) {
