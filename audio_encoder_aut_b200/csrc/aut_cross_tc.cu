@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(sm);
             constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4, kAtom16 = Cfg::kAtom >> 4;
             // The wait for a slot belongs to its first user, its release to its last.
-            auto issue_s = [&](int j, int rt) -> bool {
-                if (rt == 0 && !mbar_wait_warp(full + ki, kp, abort_v, lim)) return false;
-                tc_fence_after();
+            auto wait_k = [&] { return mbar_wait_warp(full + ki, kp, abort_v, lim); };
+            auto wait_v = [&] { return mbar_wait_warp(full + vi, vp, abort_v, lim); };
+            auto issue_s = [&](int j, int rt) {
                 const uint32_t id = idesc_qk<T>(n16(j));
                 const uint64_t qd = q_desc + rt * kTile16, kd = slot_k + ki * kTile16;
                 if (leader) {
@@ -222,13 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kp ^= 1u;
                     }
                 }
-                return true;
             };
-            auto issue_pv = [&](int j, int rt) -> bool {
-                if (!mbar_wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim) ||
-                    (rt == 0 && !mbar_wait_warp(full + vi, vp, abort_v, lim)))
-                    return false;
-                tc_fence_after();
+            auto issue_pv = [&](int j, int rt) {
                 const int steps = n16(j) / 16;
                 const uint64_t vd = slot_v + vi * kTile16;
                 const uint32_t d = tmem + Cfg::kColO + rt * HD, p = tmem + Cfg::kColP + rt * Cfg::kStepP;
@@ -248,21 +243,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vp ^= 1u;
                     }
                 }
-                return true;
             };
-            bool ok = n == 0 || mbar_wait_warp(q_full, 0, abort_v, lim);
-            if (n > 0)
-                for (int rt = 0; ok && rt < n_rt; ++rt) ok = issue_s(0, rt);
-            for (int j = 0; ok && j < n; ++j)
+            bool ok = n > 0 && mbar_wait_warp(q_full, 0, abort_v, lim) && wait_k();
+            if (ok) {
+                tc_fence_after();
+                for (int rt = 0; rt < n_rt; ++rt) issue_s(0, rt);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                // V of this tile and K of the next, long there, before the wait for P.
+                ok = wait_v() && (j + 1 == n || wait_k());
                 for (int rt = 0; ok && rt < n_rt; ++rt) {
-                    if (Cfg::kEarlyS && j + 1 < n)
-                        ok = mbar_wait_warp(s_read + rt, (uint32_t)j & 1u, abort_v, lim) && issue_s(j + 1, rt);
-                    ok = ok && issue_pv(j, rt);
-                    if (!Cfg::kEarlyS && j + 1 < n) ok = ok && issue_s(j + 1, rt);
+                    if (Cfg::kEarlyS && j + 1 < n) {
+                        ok = mbar_wait_warp(s_read + rt, (uint32_t)j & 1u, abort_v, lim);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(j + 1, rt);
+                    }
+                    ok = mbar_wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(j, rt);
+                    if (!Cfg::kEarlyS && j + 1 < n) issue_s(j + 1, rt);
                 }
+            }
             // Every product the leader issued has completed before TMEM is released.
             if (leader) {
-                if (!ok) signal_abort();
+                if (!ok && n > 0) signal_abort();
                 tc_commit(mma_done);
                 mbar_wait(mma_done, 0, nullptr, lim);
             }
