@@ -78,6 +78,37 @@ constexpr uint32_t idesc_pv() {
     return idesc_qk<T>(HD) | (1u << 16);
 }
 
+// Bounded waits for this kernel's chain of short steps: a plain try_wait (which
+// suspends the thread for as long as the hardware likes) comes back 30 to 60
+// clocks sooner than one with a suspend-time hint.
+AUT_DEV bool wait_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+AUT_DEV bool wait_one(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    if (wait_try(bar, parity)) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (wait_try(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (i == 64) t0 = now;
+            if ((abort && *abort) || now - t0 > limit_ns) return false;
+        }
+    }
+}
+AUT_DEV bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity, abort, limit_ns));
+}
+
 // Maximum of a row's 128 scores, in four chains.
 AUT_DEV float row_max(const float (&v)[4][32]) {
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -169,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int t = 0;
             for (; t < 2 * n; ++t) {
                 const int i = t % kSlots;
-                if (t >= kSlots && !mbar_wait(empty + i, (uint32_t)(t / kSlots - 1) & 1u, abort_v, lim)) {
+                if (t >= kSlots && !wait_one(empty + i, (uint32_t)(t / kSlots - 1) & 1u, abort_v, lim)) {
                     ok = false;
                     break;
                 }
@@ -185,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = t - kSlots < 0 ? 0 : t - kSlots; u < t; ++u) {
                 const uint64_t used = global_timer_ns() - t0;
                 if (used < lim)
-                    mbar_wait(full + u % kSlots, (uint32_t)(u / kSlots) & 1u, nullptr, lim - used);
+                    wait_one(full + u % kSlots, (uint32_t)(u / kSlots) & 1u, nullptr, lim - used);
             }
         }
         if (warp == kSoftmaxWarps + 1) {
@@ -202,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(sm);
             constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4, kAtom16 = Cfg::kAtom >> 4;
             // The wait for a slot belongs to its first user, its release to its last.
-            auto wait_k = [&] { return mbar_wait_warp(full + ki, kp, abort_v, lim); };
-            auto wait_v = [&] { return mbar_wait_warp(full + vi, vp, abort_v, lim); };
+            auto wait_k = [&] { return wait_warp(full + ki, kp, abort_v, lim); };
+            auto wait_v = [&] { return wait_warp(full + vi, vp, abort_v, lim); };
             auto issue_s = [&](int j, int rt) {
                 const uint32_t id = idesc_qk<T>(n16(j));
                 const uint64_t qd = q_desc + rt * kTile16, kd = slot_k + ki * kTile16;
@@ -244,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            bool ok = n > 0 && mbar_wait_warp(q_full, 0, abort_v, lim) && wait_k();
+            bool ok = n > 0 && wait_warp(q_full, 0, abort_v, lim) && wait_k();
             if (ok) {
                 tc_fence_after();
                 for (int rt = 0; rt < n_rt; ++rt) issue_s(0, rt);
@@ -254,12 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_v() && (j + 1 == n || wait_k());
                 for (int rt = 0; ok && rt < n_rt; ++rt) {
                     if (Cfg::kEarlyS && j + 1 < n) {
-                        ok = mbar_wait_warp(s_read + rt, (uint32_t)j & 1u, abort_v, lim);
+                        ok = wait_warp(s_read + rt, (uint32_t)j & 1u, abort_v, lim);
                         if (!ok) break;
                         tc_fence_after();
                         issue_s(j + 1, rt);
                     }
-                    ok = mbar_wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim);
+                    ok = wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim);
                     if (!ok) break;
                     tc_fence_after();
                     issue_pv(j, rt);
@@ -270,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
                 if (!ok && n > 0) signal_abort();
                 tc_commit(mma_done);
-                mbar_wait(mma_done, 0, nullptr, lim);
+                wait_one(mma_done, 0, nullptr, lim);
             }
             __syncwarp();
         }
@@ -304,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 scale2 = make_float2(a.scale_log2e, a.scale_log2e);
         float m = -INFINITY, l = 0.f;  // the softmax's reference (unscaled) and the row's sum
         bool ok = true;
-        // Which of key tile j's keys are read, as 4 words of 32 keys.
+        // Which of key tile j's keys are read, as 4 words of 32 keys; looked at for
+        // tiles that may miss some (one tile ahead, for the mask's sake).
         auto tile_keys = [&](int j, uint32_t(&w)[4]) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -313,13 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      j < n && key < key1 && (!a.mask || a.mask[key] != 0));
             }
         };
-        uint32_t next[4];
-        tile_keys(0, next);
+        const int n_whole = a.mask ? 0 : (key1 - key0) / kN;  // tiles known to miss none
+        uint32_t next[4] = {0, 0, 0, 0};
+        if (n_whole == 0) tile_keys(0, next);
         for (int j = 0; used && j < n; ++j) {
             const uint32_t keys[4] = {next[0], next[1], next[2], next[3]};
-            const bool whole = (keys[0] & keys[1] & keys[2] & keys[3]) == 0xffffffffu;
-            tile_keys(j + 1, next);
-            if (!mbar_wait_warp(s_full + rt, (uint32_t)j & 1u, abort_v, lim)) {
+            const bool whole =
+                j < n_whole || (keys[0] & keys[1] & keys[2] & keys[3]) == 0xffffffffu;
+            if (j + 1 >= n_whole) tile_keys(j + 1, next);
+            if (!wait_warp(s_full + rt, (uint32_t)j & 1u, abort_v, lim)) {
                 ok = false;
                 break;
             }
@@ -335,9 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read + rt);
             }
-            // P into tensor memory (over S, or over the last P) and O scaled only
-            // once the previous P V is done; with P over S, this S came after it.
-            if (Cfg::kEarlyS && j > 0 && !mbar_wait_warp(pv_done + rt, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
+            // P over the last P, and O scaled, only once the last P V is done.  (With
+            // P over S, this S came after it.)
+            if (Cfg::kEarlyS && j > 0 && !wait_warp(pv_done + rt, (uint32_t)(j - 1) & 1u, abort_v, lim)) {
                 ok = false;
                 break;
             }
@@ -360,18 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
 #pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float *x = &v[2 * h + (e >> 5)][e & 31];
+                        for (int e = 0; e < 32; e += 2) {
+                            const float *x = &v[c][e];
                             top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], x[0], x[1]);
                             const float2 y = ffma2(make_float2(x[0], x[1]), scale2, neg2);
                             const float2 q = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                             s2[(e >> 1) & 1] = fadd2(s2[(e >> 1) & 1], q);
                             p[e >> 1] = pack2<T>(q.x, q.y);
                         }
-                        tmem_st32(t_p + 32 * h, p);
+                        tmem_st16u(t_p + 16 * c, p);
                     }
                     const float2 all = fadd2(s2[0], s2[1]);
                     sum = all.x + all.y;
@@ -401,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // P V, which waits for this, comes before the second's.
             if (!whole && rt == 0) {
                 const int t = 2 * j + 1, i = t % kSlots;
-                if (!mbar_wait_warp(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim)) {
+                if (!wait_warp(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim)) {
                     ok = false;
                     break;
                 }
@@ -416,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full + rt);
         }
-        if (ok && used && n > 0) ok = mbar_wait_warp(pv_done + rt, (uint32_t)(n - 1) & 1u, abort_v, lim);
+        if (ok && used && n > 0) ok = wait_warp(pv_done + rt, (uint32_t)(n - 1) & 1u, abort_v, lim);
         if (!ok && lane == 0) signal_abort();
         if (ok && active) {
             tc_fence_after();
