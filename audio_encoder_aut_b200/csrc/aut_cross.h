@@ -43,11 +43,10 @@ struct CrossSplits {
     int n, keys;  // splits, and keys of each but the last
 };
 __host__ __device__ inline CrossSplits cross_splits(int nk, int chunk) {
-    int n = (int)(((long long)nk + chunk - 1) / chunk);
-    if (n <= 1) return {1, nk};
-    const int keys = (int)((((long long)nk + n - 1) / n + 127) / 128 * 128);
-    n = (int)(((long long)nk + keys - 1) / keys);
-    return {n, keys};
+    if (nk <= chunk) return {1, nk};
+    const unsigned n = ((unsigned)nk + (unsigned)chunk - 1) / (unsigned)chunk;  // chunk <= 2^30
+    const unsigned keys = (((unsigned)nk + n - 1) / n + 127) / 128 * 128;
+    return {(int)(((unsigned)nk + keys - 1) / keys), (int)keys};
 }
 
 // The item's request: the last one that begins at or before `item`.  The whole

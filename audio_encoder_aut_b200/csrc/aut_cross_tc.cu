@@ -166,7 +166,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
+    // The item, from the parameters, while the previous kernel ends.
+    const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
+    int seq = 0;
+    if (!a.seqs) seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
     pdl_wait();  // before the tensor memory: the previous kernel's blocks have all left
+    if (a.seqs) seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
     if (warp == kSoftmaxWarps + 1) {
         tmem_alloc(tslot, kTmemCols);
         tmem_relinquish();
@@ -177,8 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();  // the next kernel's early blocks cannot take columns this one needs
     const uint32_t tmem = *tslot;
 
-    const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
-    const int seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
     const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
     const int nq = nx.q0 - s.q0, nk = nx.k0 - s.k0;
     const int rows = nq * a.group, tiles = (rows + kCrossTileRows - 1) / kCrossTileRows;
@@ -308,18 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------- softmax --
-        // Q: 16 bytes a thread, rows one after the other.
-        constexpr int kChunks = HD / 8;
-        for (int i = threadIdx.x; i < n_rt * kM * kChunks; i += 32 * kSoftmaxWarps) {
-            const int r = i / kChunks, c = i % kChunks, at = row0 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
+        // Q: 16 bytes a thread, rows one after the other; every load before the
+        // first store.
+        constexpr int kChunks = HD / 8, kLoads = 2 * kM * kChunks / (32 * kSoftmaxWarps);
+        uint4 qv[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = threadIdx.x + u * 32 * kSoftmaxWarps, at = row0 + i / kChunks;
+            qv[u] = make_uint4(0, 0, 0, 0);
             if (at < rows) {
                 const int tok = at / a.group, head = hk * a.group + at - tok * a.group;
-                v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
-                                                     (size_t)(s.q0 + tok) * a.ld_q + head * HD + c * 8);
+                qv[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
+                                                         (size_t)(s.q0 + tok) * a.ld_q + head * HD +
+                                                         i % kChunks * 8);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = threadIdx.x + u * 32 * kSoftmaxWarps, r = i / kChunks, c = i % kChunks;
             *reinterpret_cast<uint4 *>(sm + (r >> 7) * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
-                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = qv[u];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -335,24 +346,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 scale2 = make_float2(a.scale_log2e, a.scale_log2e);
         float m = -INFINITY, l = 0.f;  // the softmax's reference (unscaled) and the row's sum
         bool ok = true;
-        // Which of key tile j's keys are read, as 4 words of 32 keys; looked at for
-        // tiles that may miss some (one tile ahead, for the mask's sake).
-        auto tile_keys = [&](int j, uint32_t(&w)[4]) {
+        // Which of key tile j's keys are read, as 4 words of 32 keys, for tiles that
+        // may miss some; their mask bytes are loaded one tile ahead.
+        auto load_mask = [&](int j, uint8_t(&w)[4]) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int key = key0 + j * kN + c * 32 + lane;
-                w[c] = __ballot_sync(0xffffffffu,
-                                     j < n && key < key1 && (!a.mask || a.mask[key] != 0));
+                w[c] = j < n && key < key1 && (!a.mask || a.mask[key] != 0);
             }
         };
         const int n_whole = a.mask ? 0 : (key1 - key0) / kN;  // tiles known to miss none
-        uint32_t next[4] = {0, 0, 0, 0};
-        if (n_whole == 0) tile_keys(0, next);
+        uint8_t next[4] = {0, 0, 0, 0};
+        if (n_whole == 0) load_mask(0, next);
         for (int j = 0; used && j < n; ++j) {
-            const uint32_t keys[4] = {next[0], next[1], next[2], next[3]};
-            const bool whole =
-                j < n_whole || (keys[0] & keys[1] & keys[2] & keys[3]) == 0xffffffffu;
-            if (j + 1 >= n_whole) tile_keys(j + 1, next);
+            uint32_t keys[4] = {0, 0, 0, 0};
+            bool whole = true;
+            if (j >= n_whole) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) keys[c] = __ballot_sync(0xffffffffu, next[c] != 0);
+                whole = (keys[0] & keys[1] & keys[2] & keys[3]) == 0xffffffffu;
+            }
+            if (j + 1 >= n_whole) load_mask(j + 1, next);
             if (!wait_warp(s_full + rt, (uint32_t)j & 1u, abort_v, lim)) {
                 ok = false;
                 break;
