@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "aut_cross.h"
 #include "aut_elem.cuh"
@@ -314,16 +315,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q: 16 bytes a thread, rows one after the other; every load before the
         // first store.
         constexpr int kChunks = HD / 8, kLoads = 2 * kM * kChunks / (32 * kSoftmaxWarps);
+        constexpr int kStep = 32 * kSoftmaxWarps / kChunks;  // rows from one load to the next
         uint4 qv[kLoads];
+        {
+            const int step_tok = kStep / a.group, step_rem = kStep - step_tok * a.group;
+            int at = row0 + (int)threadIdx.x / kChunks, tok = at / a.group, rem = at - tok * a.group;
+            const T *qp = static_cast<const T *>(a.q) + (size_t)s.q0 * a.ld_q + hk * a.group * HD +
+                          threadIdx.x % kChunks * 8;
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            const int i = threadIdx.x + u * 32 * kSoftmaxWarps, at = row0 + i / kChunks;
-            qv[u] = make_uint4(0, 0, 0, 0);
-            if (at < rows) {
-                const int tok = at / a.group, head = hk * a.group + at - tok * a.group;
-                qv[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
-                                                         (size_t)(s.q0 + tok) * a.ld_q + head * HD +
-                                                         i % kChunks * 8);
+            for (int u = 0; u < kLoads; ++u) {
+                qv[u] = make_uint4(0, 0, 0, 0);
+                if (at < rows) qv[u] = *reinterpret_cast<const uint4 *>(qp + (size_t)tok * a.ld_q + rem * HD);
+                at += kStep;
+                tok += step_tok;
+                if ((rem += step_rem) >= a.group) {
+                    rem -= a.group;
+                    ++tok;
+                }
             }
         }
 #pragma unroll
@@ -472,7 +480,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool in = at < rows;
             const float inv = sp.n > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // no key: zeros
             const size_t prow = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
-            T *dst = static_cast<T *>(a.out) + (size_t)(s.q0 + tok) * a.ld_out + head * HD;
+            // Out through the warp's 32 rows of the Q tile, which every S of this row
+            // tile has read: a thread's row becomes whole lines of the warp's stores.
+            uint8_t *const box = sm + rt * Cfg::kTileBytes + quad * 32 * HD * 2;
+            char *const dst =
+                in ? (sp.n > 1 ? reinterpret_cast<char *>(a.part_o + prow * HD)
+                               : reinterpret_cast<char *>(static_cast<T *>(a.out) +
+                                                          (size_t)(s.q0 + tok) * a.ld_out + head * HD))
+                   : nullptr;
+            // 16-byte chunks lane by lane: kRowChunks to a row of `box`, `at` bytes into the row.
+            auto flush = [&](auto row_chunks, int at_bytes) {
+                constexpr int kRowChunks = decltype(row_chunks)::value;
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < kRowChunks; ++u) {
+                    const int i = u * 32 + lane, r = i / kRowChunks, c = i % kRowChunks;
+                    char *to = reinterpret_cast<char *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+                    if (to)
+                        *reinterpret_cast<uint4 *>(to + at_bytes + c * 16) =
+                            *reinterpret_cast<const uint4 *>(box + r * kRowChunks * 16 +
+                                                             ((c ^ (r & 7)) << 4));
+                }
+                __syncwarp();
+            };
 #pragma unroll
             for (int c = 0; c < HD; c += 32) {
                 float o[32];
@@ -480,20 +511,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(t_o + c, o);
                     tc_wait_ld();
                 }
-                if (in) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float w[8];
+                for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
+                if (sp.n > 1) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] = n > 0 ? o[e + i] * inv : 0.f;
-                        if (sp.n > 1)
-                            store8(a.part_o + prow * HD + c + e, w);
-                        else
-                            store8(dst + c + e, w);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4 *>(box + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    flush(std::integral_constant<int, 8>(), c * 4);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(box + lane * HD * 2 + (((c / 8 + e) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
+                                       pack2<T>(o[8 * e + 4], o[8 * e + 5]),
+                                       pack2<T>(o[8 * e + 6], o[8 * e + 7]));
                 }
-                __syncwarp();  // converged again before the next warp-wide load
             }
+            if (sp.n == 1) flush(std::integral_constant<int, kChunks>(), 0);
             if (in && sp.n > 1) a.part_ml[prow] = make_float2(m * a.scale_log2e, l);
         }
     }
