@@ -37,10 +37,13 @@
 namespace aut {
 namespace {
 
+// Small rings, so that three blocks share a SM: most requests of a batch are a step
+// or two long, and a block's start and end are then most of its time (256 requests
+// of 6 to 780 keys: 36.5 us; 65 us with 32 keys and 3 stages, one block a SM).
 constexpr int kRows = 16;    // rows of one block
 constexpr int kRowWarps = 4;
-constexpr int kKeys = 32;    // keys of a warp's block: one lane each for the mask
-constexpr int kStages = 3;   // blocks a warp holds in its ring
+constexpr int kKeys = 16;    // keys of a warp's block (at most a lane each, for the mask)
+constexpr int kStages = 2;   // blocks a warp holds in its ring
 
 template <int HD>
 struct RowsCfg {
@@ -104,7 +107,7 @@ AUT_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, 3)
     cross_rows_kernel(const __grid_constant__ CrossArgs a) {
     using Cfg = RowsCfg<HD>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     const int tile = item % tiles;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const CrossSplits sp = cross_splits(nk, a.chunk);
+    const CrossSplits sp = cross_splits(nk, a.chunk, a.unit);
     const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
     const int n_blocks = (key1 - key0 + kKeys - 1) / kKeys;  // 0 for a request without keys
 
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     // Which of block b's keys are read (lane i: key i).
     auto block_keys = [&](int b) -> uint32_t {
         const int key = key0 + b * kKeys + lane;
-        const bool in = b < n_blocks && key < key1 && (!a.mask || a.mask[key] != 0);
+        const bool in = lane < kKeys && b < n_blocks && key < key1 && (!a.mask || a.mask[key] != 0);
         return __ballot_sync(0xffffffffu, in);
     };
     constexpr int kChunks = HD / 8;         // 16-byte chunks of a row
@@ -158,6 +161,13 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         copy_commit();
     };
 
+    uint32_t keys[kStages];  // of the blocks in the ring
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        keys[i] = block_keys(warp + i * kRowWarps);
+        copy_block(warp + i * kRowWarps, keys[i], i);
+    }
+    uint32_t ahead = block_keys(warp + (kStages - 1) * kRowWarps);
     // Queries as product operands: rows g and g + 8, columns 16 c + 2 t (+ 8).
     uint32_t qf[HD / 16][4];
 #pragma unroll
@@ -178,13 +188,6 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8; l: this lane's share
 
-    uint32_t keys[kStages];  // of the blocks in the ring
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        keys[i] = block_keys(warp + i * kRowWarps);
-        copy_block(warp + i * kRowWarps, keys[i], i);
-    }
-    uint32_t ahead = block_keys(warp + (kStages - 1) * kRowWarps);
     int stage = 0;
     for (int b = warp; b < n_blocks; b += kRowWarps) {
         {  // the block kStages - 1 ahead, into the stage the previous step has read
@@ -319,42 +322,78 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     }
 }
 
-// Adds the splits of every row of the split requests: a warp per row, HD / 8
-// lanes of it with 8 columns each.
+// Adds the splits of every row of the split requests.  HD / 8 threads take a row's
+// columns, 8 each; `groups` such teams share a row's splits (a.join_groups, a power
+// of two: one team reading 49 splits one after the other took 7 us) and meet in
+// shared memory, each time in the same order.
+constexpr int kJoinThreads = 256;
+
+int join_groups(int splits, int hd) {
+    int g = 1;
+    while (g * 2 < splits && g < kJoinThreads / (hd / 8)) g *= 2;
+    return g;
+}
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ CrossArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_constant__ CrossArgs a) {
+    constexpr int kLanes = HD / 8, kTeams = kJoinThreads / kLanes;
+    __shared__ float4 team_v[kTeams][kLanes][2];
+    __shared__ float2 team_ml[kTeams];
     pdl_trigger();
     pdl_wait();
-    constexpr int kLanes = HD / 8, kRowsAtOnce = 32 / kLanes;
-    const int warp = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, team = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    const int groups = a.join_groups, g = team % groups;
+    const int first = (int)blockIdx.x * (kTeams / groups), item = first + team / groups;
     const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
-    const int first = warp * kRowsAtOnce;
-    if (first >= a.items) return;
-    // Each lane's row may belong to another request than the warp's first.
+    // The block's rows may belong to several requests.
     int seq = cross_find(seqs, a.n_seq, first, lane);
-    const int item = first + lane / kLanes, c = lane % kLanes;
-    if (item >= a.items) return;
-    while (seqs[seq + 1].item <= item) ++seq;
+    const bool in = item < a.items;
+    while (in && seqs[seq + 1].item <= item) ++seq;
     const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
-    const int nq = nx.q0 - s.q0, splits = (nx.part - s.part) / (nq * a.heads_q);
-    const int r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
+    const int nq = nx.q0 - s.q0, r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
+    const int splits = in ? (nx.part - s.part) / (nq * a.heads_q) : 0;
     const size_t step = (size_t)nq * a.heads_q, row0 = (size_t)s.part + r;
-    float mx = -INFINITY;
-    for (int i = 0; i < splits; ++i) mx = fmaxf(mx, a.part_ml[row0 + i * step].x);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, v[8];
+    float mx = -INFINITY, sum = 0.f, v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < splits; ++i) {
+    for (int i = g; i < splits; i += groups) {
         const float2 ml = a.part_ml[row0 + i * step];
         float w[8];
         load8(a.part_o + (row0 + i * step) * HD + 8 * c, w);
-        const float f = ex2_approx(ml.x - base);
-        sum = fmaf(f, ml.y, sum);
+        const float mn = fmaxf(mx, ml.x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2_approx(mx - base), h = ex2_approx(ml.x - base);
+        mx = mn;
+        sum = sum * f + ml.y * h;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(f, w[e], v[e]);
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * f + w[e] * h;
     }
+    if (groups > 1) {
+        team_v[team][c][0] = make_float4(v[0], v[1], v[2], v[3]);
+        team_v[team][c][1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (c == 0) team_ml[team] = make_float2(mx, sum);
+        __syncthreads();
+        if (g != 0) return;
+        for (int t = team; t < team + groups; ++t) mx = fmaxf(mx, team_ml[t].x);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int t = team; t < team + groups; ++t) {
+            const float f = ex2_approx(team_ml[t].x - base);
+            const float4 x = team_v[t][c][0], y = team_v[t][c][1];
+            sum = fmaf(f, team_ml[t].y, sum);
+            v[0] = fmaf(f, x.x, v[0]);
+            v[1] = fmaf(f, x.y, v[1]);
+            v[2] = fmaf(f, x.z, v[2]);
+            v[3] = fmaf(f, x.w, v[3]);
+            v[4] = fmaf(f, y.x, v[4]);
+            v[5] = fmaf(f, y.y, v[5]);
+            v[6] = fmaf(f, y.z, v[6]);
+            v[7] = fmaf(f, y.w, v[7]);
+        }
+    }
+    if (!in) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= inv;
@@ -366,14 +405,19 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 // The kernels a request may run on, and the join after them.
 enum { kRowsKernel = 0, kTilesKernel = 1, kJoin = 2, kLists = 3 };
 
-// Blocks the splits of one kernel aim for (two a SM, or one), and the fewest
-// keys worth a split of their own.
-constexpr int kTargetItems[2] = {2 * 148, 148};
-constexpr int kMinChunk[2] = {512, 512};
+// Blocks the splits of one kernel aim for (three a SM, or one), the fewest keys
+// worth a split of their own, and the keys a split is rounded to (whole steps of
+// the row kernel's four warps; whole tiles).  One token on 15600 keys, 8 key heads
+// of 128: 14.8 us with these, 17.2 us with splits of 512, 22.5 us with one block
+// a SM.
+constexpr int kTargetItems[2] = {3 * 148, 148};
+constexpr int kMinChunk[2] = {256, 512};
+constexpr int kUnit[2] = {kRowWarps * kKeys, kCrossTileKeys};
 
 struct CrossPlan {
     int64_t items[kLists] = {0, 0, 0};  // of each kernel; of the join: rows of split requests
     int64_t part_rows = 0;              // partial rows
+    int max_splits = 1;
     int chunk[2] = {0, 0};              // keys of a split
 };
 
@@ -418,17 +462,18 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
     for (int kernel = 0; kernel < 2; ++kernel) {
         const int64_t share = (work[kernel] + kTargetItems[kernel] - 1) / kTargetItems[kernel];
         p->chunk[kernel] = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk[kernel]), 1 << 30);
-        p->chunk[kernel] = (p->chunk[kernel] + 127) / 128 * 128;
+        p->chunk[kernel] = (p->chunk[kernel] + kUnit[kernel] - 1) / kUnit[kernel] * kUnit[kernel];
     }
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
         const int kernel = kernel_of(nq, group, hd);
-        const int64_t splits = cross_splits((int)nk, p->chunk[kernel]).n;
+        const int64_t splits = cross_splits((int)nk, p->chunk[kernel], kUnit[kernel]).n;
         p->items[kernel] += split_items(kernel, nq, group, heads_kv) * splits;
         if (splits > 1) {
             p->items[kJoin] += nq * heads_q;
             p->part_rows += nq * heads_q * splits;
+            p->max_splits = std::max(p->max_splits, (int)splits);
         }
     }
     if (p->part_rows > 0x7fffffffll) return AUT_ERR_UNSUPPORTED;
@@ -448,7 +493,7 @@ void fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int hea
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
         const int kernel = kernel_of(nq, group, hd);
-        const int64_t splits = cross_splits((int)nk, p.chunk[kernel]).n;
+        const int64_t splits = cross_splits((int)nk, p.chunk[kernel], kUnit[kernel]).n;
         if (list == kernel)
             item += split_items(kernel, nq, group, heads_kv) * splits;
         else if (list == kJoin && splits > 1)
@@ -486,9 +531,9 @@ cudaError_t launch_rows(const CrossArgs &a, cudaStream_t st) {
 
 template <typename T, int HD>
 cudaError_t launch_join(const CrossArgs &a, cudaStream_t st) {
-    constexpr int rows_a_block = 8 * (32 / (HD / 8));
-    return launch_pdl(cross_join_kernel<T, HD>, dim3((unsigned)((a.items + (int64_t)rows_a_block - 1) / rows_a_block)),
-                      dim3(256), 0, st, 1, a);
+    const int rows = kJoinThreads / (HD / 8) / a.join_groups;  // of a block
+    return launch_pdl(cross_join_kernel<T, HD>, dim3((unsigned)((a.items + (int64_t)rows - 1) / rows)),
+                      dim3(kJoinThreads), 0, st, 1, a);
 }
 
 template <typename T>
@@ -574,6 +619,8 @@ extern "C" aut_status aut_cross_attention(
         if (p.items[i] == 0) continue;
         a.items = (int)p.items[i];
         a.chunk = i == kJoin ? 0 : p.chunk[i];
+        a.unit = i == kJoin ? 0 : kUnit[i];
+        a.join_groups = join_groups(p.max_splits, head_dim);
         fill_seqs(list, i, p, heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
         a.seqs = nullptr;
         if (listed) {

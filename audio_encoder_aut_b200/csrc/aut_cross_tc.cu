@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = item % tiles * kCrossTileRows;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const CrossSplits sp = cross_splits(nk, a.chunk);
+    const CrossSplits sp = cross_splits(nk, a.chunk, a.unit);
     const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
     const int n = (key1 - key0 + kN - 1) / kN;  // key tiles; 0 for a request without keys
     const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
