@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "aut_elem.cuh"
 #include "aut_internal.h"
 #include "aut_kernels.h"
@@ -16,23 +18,107 @@ namespace {
 // ---------------------------------------------------------------- quantise --
 // scale = max |x| / 127, q = rint(x / scale): the row's maximum first, then the
 // row again, so a row is kept in registers between the two (up to 64 elements a
-// thread; the rest of a longer row is read a second time).  Bound by HBM: one
-// read of x, one write of q.
+// thread; the rest of a longer row is read a second time).  Bound by HBM, one read
+// of x and one write of q, as long as an element costs no more than about ten
+// instructions and none on the conversion pipe: the maximum is taken on the bits,
+// two 16-bit elements at a time, and rounding is an addition.
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantChunks = 8;  // 8-element chunks a thread keeps
 
-// x / scale rounded to nearest even, clamped to +-127.  The quotient is taken as
-// x * inv, off by less than 2e-5 for |x / scale| <= 127 (two roundings of 2^-24 and
-// the reciprocal's); only a quotient within 1e-4 of a rounding border (or one
-// that a denormal scale spoils) needs the division itself.
-AUT_DEV int quantise(float x, float scale, float inv) {
-    float r = x * inv;
-    if (!(fabsf(fabsf(r - floorf(r)) - 0.5f) > 1e-4f) || !(fabsf(r) < 128.f)) r = x / scale;
-    return max(-127, min(127, __float2int_rn(r)));
+// A chunk as it is in memory.
+template <typename T>
+struct Raw {
+    uint32_t w[4];  // two elements each
+    AUT_DEV void load(const T *p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x;
+        w[1] = u.y;
+        w[2] = u.z;
+        w[3] = u.w;
+    }
+    // max(top, |elements|) as bits, two 16-bit halves: their order is the values',
+    // infinity above every number and NaN above that.
+    AUT_DEV uint32_t top(uint32_t t) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+        return t;
+    }
+    static AUT_DEV uint32_t fold(uint32_t t) { return max(t & 0xffffu, t >> 16); }
+    AUT_DEV void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = pair(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+    static AUT_DEV float2 pair(uint32_t u) {
+        if constexpr (std::is_same<T, __half>::value)
+            return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+        else
+            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+    static AUT_DEV float value(uint32_t bits) { return pair(bits).x; }
+};
+template <>
+struct Raw<float> {
+    uint32_t w[8];
+    AUT_DEV void load(const float *p) {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        w[0] = a.x;
+        w[1] = a.y;
+        w[2] = a.z;
+        w[3] = a.w;
+        w[4] = b.x;
+        w[5] = b.y;
+        w[6] = b.z;
+        w[7] = b.w;
+    }
+    AUT_DEV uint32_t top(uint32_t t) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, w[i] & 0x7fffffffu);
+        return t;
+    }
+    static AUT_DEV uint32_t fold(uint32_t t) { return t; }
+    AUT_DEV void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+    static AUT_DEV float value(uint32_t bits) { return __uint_as_float(bits); }
+};
+
+// Eight values / scale, rounded to nearest even, as bytes.  The quotient is taken as
+// x * inv, off by less than 4e-5 for |x / scale| <= 127 (the reciprocal's rounding, the
+// product's and the quotient's, each 2^-24 of it); adding 1.5 2^23 rounds it and
+// leaves the integer in the low bits.  Only where a quotient lies within 1e-4 of a
+// rounding border (or a denormal scale has spoilt it) are the eight divided.
+AUT_DEV uint2 quantise8(const float (&x)[8], float scale, float inv) {
+    constexpr float kMagic = 12582912.f;
+    float t[8], off = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float r = x[e] * inv;
+        t[e] = r + kMagic;
+        off = fmaxf(off, fabsf(r - (t[e] - kMagic)));
+    }
+    // An infinite inv or product is no distance from its own rounding: refused by
+    // the scale's own size.
+    if (off > 0.4999f || scale < 1e-37f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = fmaxf(-127.f, fminf(127.f, x[e] / scale)) + kMagic;
+    }
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t a = __byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040);
+        const uint32_t b = __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040);
+        o[h] = __byte_perm(a, b, 0x5410);
+    }
+    return make_uint2(o[0], o[1]);
 }
 
-// W warps per row: one (8 rows a block, no block barrier) or eight (a block a row).
+// W warps per row, 8 / W rows a block.
 template <typename T, int W>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
     const T *__restrict__ x, long long ld, int M, int K, int8_t *__restrict__ q,
@@ -42,57 +128,50 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
     pdl_wait();
     const int warp = threadIdx.x >> 5;
     constexpr int kStep = W * 32;  // chunks one pass of the row's threads covers
-    const int row = W == 1 ? (int)blockIdx.x * (kQuantThreads / 32) + warp : (int)blockIdx.x;
-    if (row >= M) return;  // whole warps; with W = 8 the grid is exact
+    const int team = warp / W, row = (int)blockIdx.x * (kQuantThreads / 32 / W) + team;
+    if (row >= M) return;  // whole teams
     const int t = threadIdx.x & (kStep - 1), chunks = K / 8;
     const T *xr = x + (size_t)row * ld;
-    float v[kQuantChunks][8];
-    // |x| as bits: their order is the values', infinities above every number
-    // and NaN above those.
+    Raw<T> v[kQuantChunks];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kQuantChunks; ++i) {
         const int c = t + i * kStep;
-        if (c < chunks) load8(xr + c * 8, v[i]);
+        if (c < chunks) v[i].load(xr + c * 8);
     }
 #pragma unroll
     for (int i = 0; i < kQuantChunks; ++i)
-        if (t + i * kStep < chunks)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
+        if (t + i * kStep < chunks) top = v[i].top(top);
     for (int c = t + kQuantChunks * kStep; c < chunks; c += kStep) {
-        float w[8];
-        load8(xr + c * 8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(w[e]) & 0x7fffffffu);
+        Raw<T> w;
+        w.load(xr + c * 8);
+        top = w.top(top);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    top = __reduce_max_sync(0xffffffffu, Raw<T>::fold(top));
     if constexpr (W > 1) {
         if ((threadIdx.x & 31) == 0) warp_max[warp] = top;
-        __syncthreads();
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
 #pragma unroll
-        for (int w = 0; w < W; ++w) top = max(top, warp_max[w]);
+        for (int w = 0; w < W; ++w) top = max(top, warp_max[team * W + w]);
     }
-    const float amax = __uint_as_float(top);
-    const bool finite = top < 0x7f800000u;
+    const float amax = Raw<T>::value(top);
+    const bool finite = amax < INFINITY;
     const float s = finite ? amax / 127.f : amax;
     if (t == 0) scale[row] = s;
     const bool zero = !finite || s == 0.f;
     const float inv = 1.f / s;
-    auto store = [&](int c, const float(&w)[8]) {
-        uint32_t o[2] = {0, 0};
-        if (!zero)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o[e >> 2] |= (uint32_t)(quantise(w[e], s, inv) & 255) << (8 * (e & 3));
-        *reinterpret_cast<uint2 *>(q + (size_t)row * K + c * 8) = make_uint2(o[0], o[1]);
+    int8_t *qr = q + (size_t)row * K;
+    auto store = [&](int c, const Raw<T> &raw) {
+        float f[8];
+        raw.values(f);
+        *reinterpret_cast<uint2 *>(qr + c * 8) = zero ? make_uint2(0, 0) : quantise8(f, s, inv);
     };
 #pragma unroll
     for (int i = 0; i < kQuantChunks; ++i)
         if (t + i * kStep < chunks) store(t + i * kStep, v[i]);
     for (int c = t + kQuantChunks * kStep; c < chunks; c += kStep) {
-        float w[8];
-        load8(xr + c * 8, w);
+        Raw<T> w;
+        w.load(xr + c * 8);
         store(c, w);
     }
 }
@@ -100,15 +179,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
 template <typename T>
 cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, void *scale,
                             cudaStream_t st) {
-    const T *xp = static_cast<const T *>(x);
-    int8_t *qp = static_cast<int8_t *>(q);
-    float *sp = static_cast<float *>(scale);
-    // One warp a row once that alone fills the GPU and the row fits its registers.
-    if (M >= 8 * sm_count_cached() && K <= 32 * 8 * kQuantChunks)
-        return launch_pdl(quantize_rows_kernel<T, 1>, dim3((M + 7) / 8), dim3(kQuantThreads), 0, st,
-                          1, xp, ld, M, K, qp, sp);
-    return launch_pdl(quantize_rows_kernel<T, 8>, dim3(M), dim3(kQuantThreads), 0, st, 1, xp, ld, M,
-                      K, qp, sp);
+    const auto go = [&](auto kernel, int rows) {
+        return launch_pdl(kernel, dim3((M + rows - 1) / rows), dim3(kQuantThreads), 0, st, 1,
+                          static_cast<const T *>(x), ld, M, K, static_cast<int8_t *>(q),
+                          static_cast<float *>(scale));
+    };
+    // The fewest warps a row that keep it in registers (8192 elements: four), so
+    // that more rows are in flight; all eight while there are too few rows to
+    // fill the GPU otherwise.
+    if (M >= 8 * sm_count_cached()) {
+        if (K <= 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 1>, 8);
+        if (K <= 2 * 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 2>, 4);
+        if (K <= 4 * 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 4>, 2);
+    }
+    return go(quantize_rows_kernel<T, 8>, 1);
 }
 
 // ------------------------------------------------- product for a few tokens --
