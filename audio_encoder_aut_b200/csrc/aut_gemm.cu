@@ -183,6 +183,17 @@ GemmStatus launch_linear(const LinearLaunch &L, cudaStream_t st) {
     int bn = 0, cg = 1;
     choose_tile(L.M, L.N, sm_count(), !L.single_cta, &bn, &cg);
     if (!bn) return GemmStatus::kBadShape;
+    if (i8 && cg == 2) {
+        // A product that single CTAs finish in one wave is too short to win back
+        // a pair's start (8-bit, 390 x 2048 x 1024: 6.6 us on 128 x 64 tiles of
+        // single CTAs, 7.8 us on pairs).
+        int bn1 = 0, cg1 = 1;
+        choose_tile(L.M, L.N, sm_count(), false, &bn1, &cg1);
+        if ((long)((L.M + 127) / 128) * (L.N / bn1) <= sm_count()) {
+            bn = bn1;
+            cg = 1;
+        }
+    }
     CUtensorMap ta, tb;
     const cuuint64_t da[2] = {(cuuint64_t)L.K, (cuuint64_t)L.M};
     const cuuint32_t kel = i8 ? 128 : 64;  // K elements of a k-block: 128 bytes

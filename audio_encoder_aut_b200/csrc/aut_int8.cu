@@ -17,14 +17,13 @@ namespace {
 
 // ---------------------------------------------------------------- quantise --
 // scale = max |x| / 127, q = rint(x / scale): the row's maximum first, then the
-// row again, so a row is kept in registers between the two (up to 64 elements a
-// thread; the rest of a longer row is read a second time).  Bound by HBM, one read
+// row again, so a row is kept in registers between the two (the rest of a row too
+// long for them is read a second time).  Bound by HBM, one read
 // of x and one write of q, as long as an element costs no more than about ten
 // instructions and none on the conversion pipe: the maximum is taken on the bits,
 // two 16-bit elements at a time, and rounding is an addition.
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantChunks = 8;  // 8-element chunks a thread keeps
 
 // A chunk as it is in memory.
 template <typename T>
@@ -118,9 +117,9 @@ AUT_DEV uint2 quantise8(const float (&x)[8], float scale, float inv) {
     return make_uint2(o[0], o[1]);
 }
 
-// W warps per row, 8 / W rows a block.
-template <typename T, int W>
-__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
+// W warps per row, 8 / W rows a block; a thread keeps C chunks of 8 elements.
+template <typename T, int W, int C>
+__global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_kernel(
     const T *__restrict__ x, long long ld, int M, int K, int8_t *__restrict__ q,
     float *__restrict__ scale) {
     __shared__ uint32_t warp_max[kQuantThreads / 32];
@@ -132,17 +131,17 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
     if (row >= M) return;  // whole teams
     const int t = threadIdx.x & (kStep - 1), chunks = K / 8;
     const T *xr = x + (size_t)row * ld;
-    Raw<T> v[kQuantChunks];
+    Raw<T> v[C];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kQuantChunks; ++i) {
+    for (int i = 0; i < C; ++i) {
         const int c = t + i * kStep;
         if (c < chunks) v[i].load(xr + c * 8);
     }
 #pragma unroll
-    for (int i = 0; i < kQuantChunks; ++i)
+    for (int i = 0; i < C; ++i)
         if (t + i * kStep < chunks) top = v[i].top(top);
-    for (int c = t + kQuantChunks * kStep; c < chunks; c += kStep) {
+    for (int c = t + C * kStep; c < chunks; c += kStep) {
         Raw<T> w;
         w.load(xr + c * 8);
         top = w.top(top);
@@ -167,9 +166,9 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
         *reinterpret_cast<uint2 *>(qr + c * 8) = zero ? make_uint2(0, 0) : quantise8(f, s, inv);
     };
 #pragma unroll
-    for (int i = 0; i < kQuantChunks; ++i)
+    for (int i = 0; i < C; ++i)
         if (t + i * kStep < chunks) store(t + i * kStep, v[i]);
-    for (int c = t + kQuantChunks * kStep; c < chunks; c += kStep) {
+    for (int c = t + C * kStep; c < chunks; c += kStep) {
         Raw<T> w;
         w.load(xr + c * 8);
         store(c, w);
@@ -184,15 +183,18 @@ cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, 
                           static_cast<const T *>(x), ld, M, K, static_cast<int8_t *>(q),
                           static_cast<float *>(scale));
     };
-    // The fewest warps a row that keep it in registers (8192 elements: four), so
-    // that more rows are in flight; all eight while there are too few rows to
-    // fill the GPU otherwise.
+    // All eight warps to a row while there are too few rows to fill the GPU
+    // otherwise (390 x 1024 bf16: 2.1 us); else the fewest that keep it in their
+    // registers, so that more rows are in flight: fp32 in 4 chunks a thread
+    // (15600 x 1280: 19.2 us, 24.0 us in 8), 16-bit types in 8 (14.4 us, 15.3 us in
+    // 4: a row of 1280 then takes two warps and a barrier).
+    constexpr int C = sizeof(T) == 4 ? 4 : 8;
     if (M >= 8 * sm_count_cached()) {
-        if (K <= 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 1>, 8);
-        if (K <= 2 * 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 2>, 4);
-        if (K <= 4 * 32 * 8 * kQuantChunks) return go(quantize_rows_kernel<T, 4>, 2);
+        if (K <= 32 * 8 * C) return go(quantize_rows_kernel<T, 1, C>, 8);
+        if (K <= 2 * 32 * 8 * C) return go(quantize_rows_kernel<T, 2, C>, 4);
+        if (K <= 4 * 32 * 8 * C) return go(quantize_rows_kernel<T, 4, C>, 2);
     }
-    return go(quantize_rows_kernel<T, 8>, 1);
+    return go(quantize_rows_kernel<T, 8, 4>, 1);
 }
 
 // ------------------------------------------------- product for a few tokens --
