@@ -6,40 +6,63 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "aut_ptx.cuh"
 
 namespace aut {
 
-AUT_DEV void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // bf16 is the upper half of the fp32 word
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight elements as they are in memory.
+template <typename T>
+struct Pack8 {
+    uint32_t w[4];  // two 16-bit elements each
+    AUT_DEV void load(const T *p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x;
+        w[1] = u.y;
+        w[2] = u.z;
+        w[3] = u.w;
     }
-}
-AUT_DEV void load8(const __half *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    AUT_DEV void values(float (&v)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = pair(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
     }
-}
-AUT_DEV void load8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0];
-    const float4 b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = a.z;
-    v[3] = a.w;
-    v[4] = b.x;
-    v[5] = b.y;
-    v[6] = b.z;
-    v[7] = b.w;
+    static AUT_DEV float2 pair(uint32_t u) {
+        if constexpr (std::is_same<T, __half>::value)
+            return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+        else  // bf16 is the upper half of the fp32 word
+            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+};
+template <>
+struct Pack8<float> {
+    uint32_t w[8];
+    AUT_DEV void load(const float *p) {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        w[0] = a.x;
+        w[1] = a.y;
+        w[2] = a.z;
+        w[3] = a.w;
+        w[4] = b.x;
+        w[5] = b.y;
+        w[6] = b.z;
+        w[7] = b.w;
+    }
+    AUT_DEV void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+};
+
+template <typename T>
+AUT_DEV void load8(const T *p, float (&v)[8]) {
+    Pack8<T> r;
+    r.load(p);
+    r.values(v);
 }
 
 // Two fp32 values as a packed pair of 16-bit ones, rounded to nearest even.

@@ -27,7 +27,7 @@
 namespace aut {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kMaxPairs = 128;  // head_dim 256
 
 struct Side {
@@ -51,7 +51,7 @@ struct NormRopeArgs {
 
 // G lanes per head: head_dim = 16 G.
 template <typename TX, typename TY, int G>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 6)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     constexpr int HD = 16 * G, kHeads = 32 / G;  // heads a warp handles at a time
     __shared__ unsigned long long turn[HD / 2];

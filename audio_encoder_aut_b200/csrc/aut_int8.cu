@@ -5,8 +5,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
 #include "aut_elem.cuh"
 #include "aut_internal.h"
 #include "aut_kernels.h"
@@ -25,67 +23,30 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 
-// A chunk as it is in memory.
+// max(top, |elements|) as bits, for 16-bit types two halves at a time: their order is
+// the values', infinity above every number and NaN above that.
 template <typename T>
-struct Raw {
-    uint32_t w[4];  // two elements each
-    AUT_DEV void load(const T *p) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        w[0] = u.x;
-        w[1] = u.y;
-        w[2] = u.z;
-        w[3] = u.w;
-    }
-    // max(top, |elements|) as bits, two 16-bit halves: their order is the values',
-    // infinity above every number and NaN above that.
-    AUT_DEV uint32_t top(uint32_t t) const {
+AUT_DEV uint32_t top_bits(const Pack8<T> &r, uint32_t t) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
-        return t;
-    }
-    static AUT_DEV uint32_t fold(uint32_t t) { return max(t & 0xffffu, t >> 16); }
-    AUT_DEV void values(float (&v)[8]) const {
+        for (int i = 0; i < 8; ++i) t = max(t, r.w[i] & 0x7fffffffu);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = pair(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
+        for (int i = 0; i < 4; ++i) t = __vmaxu2(t, r.w[i] & 0x7fff7fffu);
     }
-    static AUT_DEV float2 pair(uint32_t u) {
-        if constexpr (std::is_same<T, __half>::value)
-            return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-        else
-            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-    }
-    static AUT_DEV float value(uint32_t bits) { return pair(bits).x; }
-};
-template <>
-struct Raw<float> {
-    uint32_t w[8];
-    AUT_DEV void load(const float *p) {
-        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
-        w[0] = a.x;
-        w[1] = a.y;
-        w[2] = a.z;
-        w[3] = a.w;
-        w[4] = b.x;
-        w[5] = b.y;
-        w[6] = b.z;
-        w[7] = b.w;
-    }
-    AUT_DEV uint32_t top(uint32_t t) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t = max(t, w[i] & 0x7fffffffu);
-        return t;
-    }
-    static AUT_DEV uint32_t fold(uint32_t t) { return t; }
-    AUT_DEV void values(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    }
-    static AUT_DEV float value(uint32_t bits) { return __uint_as_float(bits); }
-};
+    return t;
+}
+template <typename T>
+AUT_DEV uint32_t fold_bits(uint32_t t) {
+    return sizeof(T) == 4 ? t : max(t & 0xffffu, t >> 16);
+}
+template <typename T>
+AUT_DEV float bits_value(uint32_t t) {
+    if constexpr (sizeof(T) == 4)
+        return __uint_as_float(t);
+    else
+        return Pack8<T>::pair(t).x;
+}
 
 // Eight values / scale, rounded to nearest even, as bytes.  The quotient is taken as
 // x * inv, off by less than 4e-5 for |x / scale| <= 127 (the reciprocal's rounding, the
@@ -131,7 +92,7 @@ __global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_k
     if (row >= M) return;  // whole teams
     const int t = threadIdx.x & (kStep - 1), chunks = K / 8;
     const T *xr = x + (size_t)row * ld;
-    Raw<T> v[C];
+    Pack8<T> v[C];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -140,27 +101,27 @@ __global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_k
     }
 #pragma unroll
     for (int i = 0; i < C; ++i)
-        if (t + i * kStep < chunks) top = v[i].top(top);
+        if (t + i * kStep < chunks) top = top_bits(v[i], top);
     for (int c = t + C * kStep; c < chunks; c += kStep) {
-        Raw<T> w;
+        Pack8<T> w;
         w.load(xr + c * 8);
-        top = w.top(top);
+        top = top_bits(w, top);
     }
-    top = __reduce_max_sync(0xffffffffu, Raw<T>::fold(top));
+    top = __reduce_max_sync(0xffffffffu, fold_bits<T>(top));
     if constexpr (W > 1) {
         if ((threadIdx.x & 31) == 0) warp_max[warp] = top;
         asm volatile("barrier.cta.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
 #pragma unroll
         for (int w = 0; w < W; ++w) top = max(top, warp_max[team * W + w]);
     }
-    const float amax = Raw<T>::value(top);
+    const float amax = bits_value<T>(top);
     const bool finite = amax < INFINITY;
     const float s = finite ? amax / 127.f : amax;
     if (t == 0) scale[row] = s;
     const bool zero = !finite || s == 0.f;
     const float inv = 1.f / s;
     int8_t *qr = q + (size_t)row * K;
-    auto store = [&](int c, const Raw<T> &raw) {
+    auto store = [&](int c, const Pack8<T> &raw) {
         float f[8];
         raw.values(f);
         *reinterpret_cast<uint2 *>(qr + c * 8) = zero ? make_uint2(0, 0) : quantise8(f, s, inv);
@@ -169,7 +130,7 @@ __global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_k
     for (int i = 0; i < C; ++i)
         if (t + i * kStep < chunks) store(t + i * kStep, v[i]);
     for (int c = t + C * kStep; c < chunks; c += kStep) {
-        Raw<T> w;
+        Pack8<T> w;
         w.load(xr + c * 8);
         store(c, w);
     }
