@@ -301,11 +301,14 @@ def aut_inject_workspace_bytes(L: int) -> int:
 
 
 def _offsets(values):
-    """(address, entries, owner) of int32 offsets for a call: a contiguous int32 array
-    (numpy's, say) is passed as it is, anything else is copied to one."""
-    face = getattr(values, "__array_interface__", None)
-    if face and face["typestr"] == "<i4" and not face.get("strides") and len(face["shape"]) == 1:
-        return face["data"][0], face["shape"][0], values
+    """(address, entries, owner) of int32 offsets for a call: a writable contiguous int32
+    buffer (a numpy array, say) is passed as it is, anything else is copied to one."""
+    try:
+        view = memoryview(values)
+        if view.format == "i" and view.ndim == 1 and view.contiguous and not view.readonly and view.shape[0]:
+            return ctypes.addressof(c_int32.from_buffer(values)), view.shape[0], values
+    except TypeError:  # no buffer
+        pass
     arr = (c_int32 * max(1, len(values)))(*[int(v) for v in values])
     return ctypes.addressof(arr), len(values), arr
 

@@ -117,15 +117,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
     const int seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
-    const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
-    const int nq = nx.q0 - s.q0, nk = nx.k0 - s.k0;
-    const int rows = nq * a.group, tiles = (rows + kRows - 1) / kRows;
+    const CrossSeq s = seqs[seq];
+    const int nq = s.nq, rows = nq * a.group, tiles = (rows + kRows - 1) / kRows;
     int item = (int)blockIdx.x - s.item;
     const int tile = item % tiles;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const CrossSplits sp = cross_splits(nk, a.chunk, a.unit);
-    const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
+    const int key0 = s.k0 + split * s.keys, key1 = min(s.k0 + s.nk, key0 + s.keys);
     const int n_blocks = (key1 - key0 + kKeys - 1) / kKeys;  // 0 for a request without keys
 
     // Row r of the tile: query (tile 16 + r) / group, head hk group + (tile 16 + r) % group.
@@ -309,7 +307,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = fmaf(f, join[(w * kRows + r) * kLd + 8 * c + e], v[e]);
         }
-        if (sp.n > 1) {
+        if (s.splits > 1) {
             const size_t row = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
             store8(a.part_o + row * HD + 8 * c, v);
             if (c == 0) a.part_ml[row] = make_float2(mx, sum);
@@ -349,10 +347,10 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
     int seq = cross_find(seqs, a.n_seq, first, lane);
     const bool in = item < a.items;
     while (in && seqs[seq + 1].item <= item) ++seq;
-    const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
-    const int nq = nx.q0 - s.q0, r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
-    const int splits = in ? (nx.part - s.part) / (nq * a.heads_q) : 0;
-    const size_t step = (size_t)nq * a.heads_q, row0 = (size_t)s.part + r;
+    const CrossSeq s = seqs[seq];
+    const int r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
+    const int splits = in ? s.splits : 0;
+    const size_t step = (size_t)s.nq * a.heads_q, row0 = (size_t)s.part + r;
     float mx = -INFINITY, sum = 0.f, v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -414,12 +412,30 @@ constexpr int kTargetItems[2] = {3 * 148, 148};
 constexpr int kMinChunk[2] = {256, 512};
 constexpr int kUnit[2] = {kRowWarps * kKeys, kCrossTileKeys};
 
+// No request of up to so many keys is split: one block then ends before a second
+// kernel has joined two (390 keys, 16 heads of 64: 4.9 us whole, 6.2 us in two).
+constexpr int kCrossWhole = 512;
+
 struct CrossPlan {
     int64_t items[kLists] = {0, 0, 0};  // of each kernel; of the join: rows of split requests
     int64_t part_rows = 0;              // partial rows
     int max_splits = 1;
-    int chunk[2] = {0, 0};              // keys of a split
+    int chunk[2] = {0, 0};              // most keys of a split
 };
+
+struct Splits {
+    int n, keys;  // splits, and keys of each but the last
+};
+
+// A request's splits: as few as the kernel's chunk allows (at least one), as even
+// as whole units of keys allow.
+Splits split_keys(int nk, int kernel, const CrossPlan &p) {
+    const unsigned chunk = (unsigned)p.chunk[kernel], unit = (unsigned)kUnit[kernel];  // chunk <= 2^30
+    if (nk <= kCrossWhole || (unsigned)nk <= chunk) return {1, nk};
+    const unsigned n = ((unsigned)nk + chunk - 1) / chunk;
+    const unsigned keys = (((unsigned)nk + n - 1) / n + unit - 1) / unit * unit;
+    return {(int)(((unsigned)nk + keys - 1) / keys), (int)keys};
+}
 
 // A request runs on the tcgen05 kernel once its rows pass one 16-row block:
 // from there on the row kernel would read the keys once per block.
@@ -468,7 +484,7 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
         const int kernel = kernel_of(nq, group, hd);
-        const int64_t splits = cross_splits((int)nk, p->chunk[kernel], kUnit[kernel]).n;
+        const int64_t splits = split_keys((int)nk, kernel, *p).n;
         p->items[kernel] += split_items(kernel, nq, group, heads_kv) * splits;
         if (splits > 1) {
             p->items[kJoin] += nq * heads_q;
@@ -482,24 +498,47 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
     return AUT_OK;
 }
 
-// The requests as kernel `list` (or the join) sees them.
-void fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int heads_kv, int hd,
-               const int32_t *cu_q, const int32_t *cu_k, int n_seq) {
+// The requests as kernel `list` (or the join) sees them: those with items, in
+// order, for the tile kernel those with long splits first (its blocks end together
+// only if the last ones are short).  Returns how many.
+int fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int heads_kv, int hd,
+              const int32_t *cu_q, const int32_t *cu_k, int n_seq) {
+    constexpr int kBuckets = 64;  // of key tiles, the last for all longer splits
     const int group = heads_q / heads_kv;
-    int64_t item = 0, part = 0;
-    for (int i = 0; i <= n_seq; ++i) {
-        out[i] = {cu_q[i], cu_k[i], (int)item, (int)part};
-        if (i == n_seq) break;
-        const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
-        if (nq == 0) continue;
-        const int kernel = kernel_of(nq, group, hd);
-        const int64_t splits = cross_splits((int)nk, p.chunk[kernel], kUnit[kernel]).n;
-        if (list == kernel)
-            item += split_items(kernel, nq, group, heads_kv) * splits;
-        else if (list == kJoin && splits > 1)
-            item += nq * heads_q;
-        if (splits > 1) part += nq * heads_q * splits;
+    int64_t items = 0, part = 0;
+    int n = 0, first[kBuckets + 1] = {0};
+    const auto bucket = [&](int keys) {
+        const int tiles = (int)(((int64_t)keys + kCrossTileKeys - 1) / kCrossTileKeys);
+        return kBuckets - 1 - std::min(tiles, kBuckets - 1);
+    };
+    const auto visit = [&](auto &&use) {
+        part = 0;
+        for (int i = 0; i < n_seq; ++i) {
+            const int nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
+            if (nq == 0) continue;
+            const int kernel = kernel_of(nq, group, hd);
+            const Splits s = split_keys(nk, kernel, p);
+            if (list == kernel || (list == kJoin && s.n > 1))
+                use(CrossSeq{cu_q[i], nq, cu_k[i], nk, 0, (int)part, s.n, s.keys});
+            if (s.n > 1) part += (int64_t)nq * heads_q * s.n;
+        }
+    };
+    if (list == kTilesKernel) {
+        visit([&](const CrossSeq &s) { ++first[bucket(s.keys) + 1]; });
+        for (int b = 0; b < kBuckets; ++b) first[b + 1] += first[b];
+        n = first[kBuckets];
+        visit([&](const CrossSeq &s) { out[first[bucket(s.keys)]++] = s; });
+    } else {
+        visit([&](const CrossSeq &s) { out[n++] = s; });
     }
+    for (int i = 0; i < n; ++i) {
+        out[i].item = (int)items;
+        items += list == kJoin ? (int64_t)out[i].nq * heads_q
+                               : split_items(list, out[i].nq, group, heads_kv) * out[i].splits;
+    }
+    out[n] = CrossSeq{};
+    out[n].item = (int)items;
+    return n;
 }
 
 struct CrossLayout {
@@ -608,7 +647,6 @@ extern "C" aut_status aut_cross_attention(
     a.scale_log2e = (float)((double)scale * 1.4426950408889634);
     a.status = reinterpret_cast<int *>(status);
     a.timeout_ns = timeout_ms ? (unsigned long long)timeout_ms * 1000000ull : 4000ull * 1000000ull;
-    a.n_seq = n_seq;
     a.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + lay.part_ml);
     const bool listed = n_seq > kCrossInline;
@@ -618,15 +656,13 @@ extern "C" aut_status aut_cross_attention(
     for (int i = 0; i < kLists && result == AUT_OK; ++i) {
         if (p.items[i] == 0) continue;
         a.items = (int)p.items[i];
-        a.chunk = i == kJoin ? 0 : p.chunk[i];
-        a.unit = i == kJoin ? 0 : kUnit[i];
         a.join_groups = join_groups(p.max_splits, head_dim);
-        fill_seqs(list, i, p, heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
+        a.n_seq = fill_seqs(list, i, p, heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
         a.seqs = nullptr;
         if (listed) {
             CrossSeq *dev = reinterpret_cast<CrossSeq *>(ws + lay.list[i]);
             a.seqs = dev;
-            if (launch_upload(reinterpret_cast<const int32_t *>(list), (size_t)(n_seq + 1) * 4,
+            if (launch_upload(reinterpret_cast<const int32_t *>(list), (size_t)(a.n_seq + 1) * (sizeof(CrossSeq) / 4),
                               reinterpret_cast<int32_t *>(dev), s) != cudaSuccess)
                 result = AUT_ERR_CUDA;
         }

@@ -10,14 +10,16 @@ namespace aut {
 
 // Up to kCrossInline requests travel in the kernels' parameters (one launch
 // less); longer lists are uploaded to the workspace.
-constexpr int kCrossInline = 512;
+constexpr int kCrossInline = 256;
 
-// One request as one kernel sees it; entry n closes the list.  Its work items
-// are item .. next item (none, if another kernel handles it): [split][key
-// head][row tile].  With more than one split its partial results are rows
-// part .. next part of the partial buffer: [split][query][query head].
+// One request as one kernel sees it; the entry behind the last one only has `item`.
+// Its work items are item .. next item (none, if another kernel handles it):
+// [split][key head][row tile].  With more than one split its partial results start
+// at row `part` of the partial buffer: [split][query][query head].
 struct CrossSeq {
-    int q0, k0, item, part;
+    int q0, nq, k0, nk;  // first row and rows of its queries and keys
+    int item, part;
+    int splits, keys;    // splits, and keys of each but the last
 };
 
 struct CrossArgs {
@@ -27,8 +29,6 @@ struct CrossArgs {
     long long ld_q, ld_k, ld_v, ld_out;  // elements
     int heads_q, heads_kv, group;
     float scale_log2e;
-    int chunk;        // most keys of a split
-    int unit;         // its keys come in multiples of this
     int n_seq, items;
     int join_groups;  // of the join: teams that share a row's splits
     float *part_o;    // [partial rows][head_dim], fp32, over each split's own row maximum
@@ -38,22 +38,6 @@ struct CrossArgs {
     const CrossSeq *seqs;  // in the workspace; null: `inline_seqs`
     CrossSeq inline_seqs[kCrossInline + 1];
 };
-
-// No request of up to so many keys is split: one block then ends before a second
-// kernel has joined two (390 keys, 16 heads of 64: 4.9 us whole, 6.2 us in two).
-constexpr int kCrossWhole = 512;
-
-// A request's splits: as few as `chunk` allows (at least one), as even as whole
-// units of keys allow.
-struct CrossSplits {
-    int n, keys;  // splits, and keys of each but the last
-};
-__host__ __device__ inline CrossSplits cross_splits(int nk, int chunk, int unit) {
-    if (nk <= chunk || nk <= kCrossWhole) return {1, nk};
-    const unsigned n = ((unsigned)nk + (unsigned)chunk - 1) / (unsigned)chunk;  // chunk <= 2^30
-    const unsigned keys = (((unsigned)nk + n - 1) / n + unit - 1) / unit * unit;
-    return {(int)(((unsigned)nk + keys - 1) / keys), (int)keys};
-}
 
 // The item's request: the last one that begins at or before `item`.  The whole
 // warp searches, 32 probes a round.

@@ -183,15 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();  // the next kernel's early blocks cannot take columns this one needs
     const uint32_t tmem = *tslot;
 
-    const CrossSeq s = seqs[seq], nx = seqs[seq + 1];
-    const int nq = nx.q0 - s.q0, nk = nx.k0 - s.k0;
-    const int rows = nq * a.group, tiles = (rows + kCrossTileRows - 1) / kCrossTileRows;
+    const CrossSeq s = seqs[seq];
+    const int nq = s.nq, rows = nq * a.group, tiles = (rows + kCrossTileRows - 1) / kCrossTileRows;
     int item = (int)blockIdx.x - s.item;
     const int row0 = item % tiles * kCrossTileRows;
     item /= tiles;
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
-    const CrossSplits sp = cross_splits(nk, a.chunk, a.unit);
-    const int key0 = s.k0 + split * sp.keys, key1 = min(nx.k0, key0 + sp.keys);
+    const int key0 = s.k0 + split * s.keys, key1 = min(s.k0 + s.nk, key0 + s.keys);
     const int n = (key1 - key0 + kN - 1) / kN;  // key tiles; 0 for a request without keys
     const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
 
@@ -478,13 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int at = row0 + rt * kM + row, tok = at / a.group, head = hk * a.group + at - tok * a.group;
             const bool in = at < rows;
-            const float inv = sp.n > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+            const float inv = s.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // no key: zeros
             const size_t prow = (size_t)s.part + ((size_t)split * nq + tok) * a.heads_q + head;
             // Out through the warp's 32 rows of the Q tile, which every S of this row
             // tile has read: a thread's row becomes whole lines of the warp's stores.
             uint8_t *const box = sm + rt * Cfg::kTileBytes + quad * 32 * HD * 2;
             char *const dst =
-                in ? (sp.n > 1 ? reinterpret_cast<char *>(a.part_o + prow * HD)
+                in ? (s.splits > 1 ? reinterpret_cast<char *>(a.part_o + prow * HD)
                                : reinterpret_cast<char *>(static_cast<T *>(a.out) +
                                                           (size_t)(s.q0 + tok) * a.ld_out + head * HD))
                    : nullptr;
@@ -513,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
-                if (sp.n > 1) {
+                if (s.splits > 1) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         *reinterpret_cast<float4 *>(box + lane * 128 + ((e ^ (lane & 7)) << 4)) =
@@ -528,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        pack2<T>(o[8 * e + 6], o[8 * e + 7]));
                 }
             }
-            if (sp.n == 1) flush(std::integral_constant<int, kChunks>(), 0);
-            if (in && sp.n > 1) a.part_ml[prow] = make_float2(m * a.scale_log2e, l);
+            if (s.splits == 1) flush(std::integral_constant<int, kChunks>(), 0);
+            if (in && s.splits > 1) a.part_ml[prow] = make_float2(m * a.scale_log2e, l);
         }
     }
     tc_fence_before();
