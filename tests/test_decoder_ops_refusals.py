@@ -71,7 +71,7 @@ def test_norm_rope_nothing_to_do():
     (dict(heads_q=1 << 20), UNS), (dict(dtype=A.F32), BAD), (dict(dtype=7), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
     (dict(scale=float("inf")), BAD), (dict(scale=float("nan")), BAD), (dict(timeout_ms=-1), BAD), (dict(cu_q=[1, 3, 9]), BAD),
     (dict(cu_k=[2, 5, 5]), BAD), (dict(cu_q=[0, 4, 3]), BAD), (dict(cu_k=[0, 9, 3]), BAD), (dict(cu_q=[0, 4]), BAD), (dict(cu_q=[]), BAD),
-    (dict(cu_q=[0, 3, 1 << 30]), UNS), (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(out=None), BAD),
+    (dict(cu_q=[0, 3, 1 << 30]), UNS), (dict(cu_k=[0, 3, (1 << 31) - 1]), UNS), (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(out=None), BAD),
     (dict(q=P + 8), BAD), (dict(k=P + 2), BAD), (dict(v=P + 8), BAD), (dict(out=P + 4), BAD), (dict(ld_q=248), BAD), (dict(ld_k=120), BAD),
     (dict(ld_v=64), BAD), (dict(ld_out=255), BAD), (dict(ld_q=260), BAD), (dict(ld_k=132), BAD), (dict(ld_q=1 << 39), BAD),
     (dict(workspace=None), BAD), (dict(workspace=P + 128), BAD), (dict(ws_bytes=0), WS), (dict(status=P + 2), BAD)])

@@ -165,6 +165,29 @@ def test_linear_i8_longest_sum(M):
     assert np.abs(_np(y) - want).max() <= 127.0 * 127 * K * R.U32
 
 
+@pytest.mark.parametrize("flags", [0, A.LINEAR_SINGLE_CTA], ids=["auto", "single_cta"])
+def test_linear_i8_wait_that_runs_out_is_reported(flags):
+    """The first block leaves its first operand load out: the kernel gives up after
+    its time limit, says so in the status word and leaves the GPU usable."""
+    M, N, K = 512, 256, 256
+    x = torch.ones(M, K, dtype=torch.int8, device="cuda")
+    w = torch.ones(N, K, dtype=torch.int8, device="cuda")
+    one = torch.ones(M, device="cuda")
+    y = torch.zeros(M, N, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(extra):
+        return A.aut_linear_i8(x.data_ptr(), one.data_ptr(), w.data_ptr(), one.data_ptr(), None, y.data_ptr(), M, N, K, A.EPI_F32,
+                               status.data_ptr(), 20, flags | extra, _stream())
+    assert call(A.LINEAR_FAULT_INJECT) == A.AUT_OK
+    torch.cuda.synchronize()
+    assert A.aut_check_status_word(status.data_ptr()) == A.AUT_ERR_TIMEOUT
+    assert call(0) == A.AUT_OK
+    torch.cuda.synchronize()
+    assert A.aut_check_status_word(status.data_ptr()) == A.AUT_OK
+    assert (y == K).all()
+
+
 def test_linear_i8_spoilt_row_is_nan_alone():
     M, N, K = 40, 32, 64
     x = _draw((M, K), "f32", 1)
@@ -362,6 +385,32 @@ def test_cross_masked_rows_may_hold_anything(q_len, hd):
     m[300:364] = 0
     m[493:493 + 260] = 0
     Cross(4, 2, hd, "bf16", [q_len] * 4, k_lens, m).check(bad_masked=True)
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("q_len", [1, 150])
+@pytest.mark.parametrize("k_len,at", [(300, 290), (9000, 4321)])
+def test_cross_keys_that_are_read_do_reach_the_result(k_len, at, q_len, hd):
+    """NaN and infinity in a key that counts spoil every query of its request and
+    key head, NaN in a query that query's head, and nothing else."""
+    for bad in (float("nan"), float("inf")):
+        c = Cross(4, 2, hd, "bf16", [q_len, q_len], [k_len, 200])
+        c.kv[at, 0] = bad           # key head 0: query heads 0 and 1 of the first request
+        c.kv[k_len + 3, hd] = 0.0
+        if bad != bad:
+            c.q[2 * q_len - 1, 3 * hd] = bad
+        assert c.call() == A.AUT_OK
+        torch.cuda.synchronize()
+        out = c.out[:2 * q_len, :4 * hd].view(2 * q_len, 4, hd)
+        spoilt = torch.isnan(out).all(-1).cpu().numpy()
+        want = np.zeros((2 * q_len, 4), bool)
+        want[:q_len, :2] = True
+        if bad != bad:
+            want[2 * q_len - 1, 3] = True
+        else:  # infinity times a negative query element is -infinity: that row's key just drops out
+            want[:q_len, :2] = (c.q[:q_len, :4 * hd].view(q_len, 4, hd)[:, :2, 0] > 0).cpu().numpy()
+        np.testing.assert_array_equal(spoilt, want)
+        assert torch.isfinite(out[torch.from_numpy(~want).cuda()]).all()
 
 
 @pytest.mark.parametrize("hd", [64, 128])
