@@ -173,16 +173,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!a.seqs) seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
     pdl_wait();  // before the tensor memory: the previous kernel's blocks have all left
     if (a.seqs) seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
-    if (warp == kSoftmaxWarps + 1) {
-        tmem_alloc(tslot, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_trigger();  // the next kernel's early blocks cannot take columns this one needs
-    const uint32_t tmem = *tslot;
-
     const CrossSeq s = seqs[seq];
     const int nq = s.nq, rows = nq * a.group, tiles = (rows + kCrossTileRows - 1) / kCrossTileRows;
     int item = (int)blockIdx.x - s.item;
@@ -192,6 +182,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key0 = s.k0 + split * s.keys, key1 = min(s.k0 + s.nk, key0 + s.keys);
     const int n = (key1 - key0 + kN - 1) / kN;  // key tiles; 0 for a request without keys
     const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
+
+            // Q: 16 bytes a thread, rows one after the other; the loads run while the block
+    // sets itself up.
+    constexpr int kChunks = HD / 8, kLoads = 2 * kM * kChunks / (32 * kSoftmaxWarps);
+    constexpr int kStep = 32 * kSoftmaxWarps / kChunks;  // rows from one load to the next
+    uint4 qv[kLoads];
+    if (warp < kSoftmaxWarps) {
+        const int step_tok = kStep / a.group, step_rem = kStep - step_tok * a.group;
+        int at = row0 + (int)threadIdx.x / kChunks, tok = at / a.group, rem = at - tok * a.group;
+        const T *qp = static_cast<const T *>(a.q) + (size_t)s.q0 * a.ld_q + hk * a.group * HD +
+                      threadIdx.x % kChunks * 8;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            qv[u] = make_uint4(0, 0, 0, 0);
+            if (at < rows) qv[u] = *reinterpret_cast<const uint4 *>(qp + (size_t)tok * a.ld_q + rem * HD);
+            at += kStep;
+            tok += step_tok;
+            if ((rem += step_rem) >= a.group) {
+                rem -= a.group;
+                ++tok;
+            }
+        }
+    }
+
+    if (warp == kSoftmaxWarps + 1) {
+        tmem_alloc(tslot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // the next kernel's early blocks cannot take columns this one needs
+    const uint32_t tmem = *tslot;
 
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -310,28 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------- softmax --
-        // Q: 16 bytes a thread, rows one after the other; every load before the
-        // first store.
-        constexpr int kChunks = HD / 8, kLoads = 2 * kM * kChunks / (32 * kSoftmaxWarps);
-        constexpr int kStep = 32 * kSoftmaxWarps / kChunks;  // rows from one load to the next
-        uint4 qv[kLoads];
-        {
-            const int step_tok = kStep / a.group, step_rem = kStep - step_tok * a.group;
-            int at = row0 + (int)threadIdx.x / kChunks, tok = at / a.group, rem = at - tok * a.group;
-            const T *qp = static_cast<const T *>(a.q) + (size_t)s.q0 * a.ld_q + hk * a.group * HD +
-                          threadIdx.x % kChunks * 8;
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                qv[u] = make_uint4(0, 0, 0, 0);
-                if (at < rows) qv[u] = *reinterpret_cast<const uint4 *>(qp + (size_t)tok * a.ld_q + rem * HD);
-                at += kStep;
-                tok += step_tok;
-                if ((rem += step_rem) >= a.group) {
-                    rem -= a.group;
-                    ++tok;
-                }
-            }
-        }
+        // Q into shared memory.
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             const int i = threadIdx.x + u * 32 * kSoftmaxWarps, r = i / kChunks, c = i % kChunks;
