@@ -421,6 +421,8 @@ struct CrossPlan {
     int64_t part_rows = 0;              // partial rows
     int max_splits = 1;
     int chunk[2] = {0, 0};              // most keys of a split
+    bool small_call = false;            // everything on the row kernel
+    bool long_prompts = false;          // some request has more than two row blocks
 };
 
 struct Splits {
@@ -437,10 +439,16 @@ Splits split_keys(int nk, int kernel, const CrossPlan &p) {
     return {(int)(((unsigned)nk + keys - 1) / keys), (int)keys};
 }
 
-// A request runs on the tcgen05 kernel once its rows pass one 16-row block:
-// from there on the row kernel would read the keys once per block.
-int kernel_of(int64_t nq, int group, int hd) {
-    return hd >= 64 && nq * group > kRows ? kTilesKernel : kRowsKernel;
+// Which kernel a request runs on.  One 16-row block is the row kernel's.  Two still
+// are: the second read of the keys (out of L2) costs less than the tile kernel's
+// longer start (16 requests of 1500 keys, 16 heads of 64, 32 rows: 35 us against
+// 46 us; 48 rows of 128: 71 us against 60 us), unless the call runs the tile kernel
+// anyway: a kernel of their own then takes longer (16 prompts, one of them of 29
+// rows: 55 us against 50 us).  On a small call, everything is the row kernel's.
+int kernel_of(int64_t nq, int group, int hd, const CrossPlan &p) {
+    const int64_t rows = nq * group;
+    if (hd < 64 || p.small_call || rows <= kRows) return kRowsKernel;
+    return rows <= 2 * kRows && !p.long_prompts ? kRowsKernel : kTilesKernel;
 }
 
 bool head_dim_ok(int hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
@@ -467,13 +475,47 @@ int64_t split_items(int kernel, int64_t nq, int group, int heads_kv) {
     return (nq * group + rows - 1) / rows * heads_kv;
 }
 
+// Whether the row kernel would end a call's requests of more than one row block
+// before the tile kernel does.  Estimates in us from what both measured over 20 to 512 rows, 100
+// to 4000 keys, 1 and 16 requests: the row kernel takes 3.3 (4.3 with head_dim
+// 128) and 19 (32) ns for every key of a block, three blocks a SM; the tile kernel
+// 5.2 (7) an item and 1.45 (2) a tile of keys, one item a SM, and 2 for a join.
+// One request, 16 heads of 64, 128 rows: 5.4 against 11.8 us on 400 keys, 25
+// against 18 us on 4000.
+bool small_call(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
+                int n_seq) {
+    const int group = heads_q / heads_kv;
+    double block_keys = 0, items = 0, tiles = 0, most = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
+        if (nq * group <= kRows) continue;
+        const double it = (double)split_items(kTilesKernel, nq, group, heads_kv);
+        const double ti = (double)((nk + kCrossTileKeys - 1) / kCrossTileKeys);
+        block_keys += (double)split_items(kRowsKernel, nq, group, heads_kv) * (double)nk;
+        items += it;
+        tiles += it * ti;
+        most = std::max(most, ti);
+    }
+    const bool wide = hd > 64;
+    const double share = tiles / 148, whole = (double)kMinChunk[kTilesKernel] / kCrossTileKeys;
+    const double rows_us =
+        (wide ? 4.3 : 3.3) + (wide ? 0.032 : 0.019) * block_keys / kTargetItems[kRowsKernel];
+    const double tiles_us = (wide ? 7.0 : 5.2) * std::max(1.0, items / 148) +
+                            (wide ? 2.0 : 1.45) * std::max(share, std::min(most, whole)) +
+                            (most > whole ? 2.0 : 0.0);
+    return rows_us < tiles_us;
+}
+
 aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
                       int n_seq, CrossPlan *p) {
     const int group = heads_q / heads_kv;
+    p->small_call = small_call(heads_q, heads_kv, hd, cu_q, cu_k, n_seq);
+    for (int i = 0; i < n_seq; ++i)
+        p->long_prompts |= (int64_t)(cu_q[i + 1] - cu_q[i]) * group > 2 * kRows;
     int64_t work[2] = {0, 0};  // keys read by all of a kernel's items, unsplit
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i];
-        const int kernel = kernel_of(nq, group, hd);
+        const int kernel = kernel_of(nq, group, hd, *p);
         work[kernel] += split_items(kernel, nq, group, heads_kv) * (cu_k[i + 1] - cu_k[i]);
     }
     // Every split about as long as one block's share of the whole.
@@ -485,7 +527,7 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;
-        const int kernel = kernel_of(nq, group, hd);
+        const int kernel = kernel_of(nq, group, hd, *p);
         const int64_t splits = split_keys((int)nk, kernel, *p).n;
         p->items[kernel] += split_items(kernel, nq, group, heads_kv) * splits;
         if (splits > 1) {
@@ -518,7 +560,7 @@ int fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int head
         for (int i = 0; i < n_seq; ++i) {
             const int nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
             if (nq == 0) continue;
-            const int kernel = kernel_of(nq, group, hd);
+            const int kernel = kernel_of(nq, group, hd, p);
             const Splits s = split_keys(nk, kernel, p);
             if (list == kernel || (list == kJoin && s.n > 1))
                 use(CrossSeq{cu_q[i], nq, cu_k[i], nk, 0, (int)part, s.n, s.keys});
