@@ -297,9 +297,15 @@ def test_norm_rope_one_side_and_zero_head():
 # -------------------------------------------------------------- cross attention
 
 class Cross:
-    """One call's inputs on the GPU; run() gives the output with sentinel rows behind it."""
+    """One call's inputs on the GPU; its output has sentinel rows behind it.  `large`: with
+    one more request behind the others, of so many rows and keys that the requests of
+    more than 32 rows (16, with head_dim 64 and 128) run on the tile kernel."""
 
-    def __init__(self, hq, hk, hd, dtype, q_lens, k_lens, mask=None, scale=None, seed=0, pad=0, qk_scale=1.0):
+    def __init__(self, hq, hk, hd, dtype, q_lens, k_lens, mask=None, scale=None, seed=0, pad=0, qk_scale=1.0, large=False):
+        if large:
+            if mask is not None and not isinstance(mask, str):
+                mask = np.concatenate([mask, np.arange(2999) % 5 != 0])
+            q_lens, k_lens = list(q_lens) + [2000 * hk // hq], list(k_lens) + [2999]
         self.hq, self.hk, self.hd, self.dtype = hq, hk, hd, dtype
         self.cu_q = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
         self.cu_k = np.concatenate([[0], np.cumsum(k_lens)]).astype(np.int32)
@@ -365,36 +371,49 @@ def test_cross_single_tokens(hq, hk, hd, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("hd", [16, 32, 64, 128])
 @pytest.mark.parametrize("mask", [None, "random"])
-def test_cross_ragged_prompts(mask, hd, dtype):
-    Cross(6, 2, hd, dtype, [0, 1, 5, 6, 43, 130, 0, 129, 257, 17], [3, 0, 1, 129, 128, 500, 40, 127, 33, 300], mask, pad=8).check()
+@pytest.mark.parametrize("large", [False, True])
+def test_cross_ragged_prompts(large, mask, hd, dtype):
+    Cross(6, 2, hd, dtype, [0, 1, 5, 6, 43, 130, 0, 129, 257, 17], [3, 0, 1, 129, 128, 500, 40, 127, 33, 300], mask, pad=8,
+          large=large).check()
 
 
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (10, 2), (16, 16)])
-def test_cross_longer_prompts(hq, hk, hd):
-    Cross(hq, hk, hd, "bf16", [300, 1, 128], [700, 1000, 385]).check()
+@pytest.mark.parametrize("large", [False, True])
+def test_cross_longer_prompts(large, hq, hk, hd):
+    Cross(hq, hk, hd, "bf16", [300, 1, 128], [700, 1000, 385], large=large).check()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_cross_prompts_of_one_to_three_row_blocks(hd):
+    """15 to 49 rows a request: on the row kernel alone, and beside longer prompts."""
+    for large in (False, True):
+        Cross(1, 1, hd, "f16", [15, 16, 17, 31, 32, 33, 48, 49], [100, 0, 300, 40, 129, 64, 1, 257], large=large).check()
+    Cross(16, 16, hd, "bf16", [32] * 16, [1500] * 16).check()  # many, none longer than two blocks
 
 
 @pytest.mark.parametrize("hd", [32, 64, 128])
 @pytest.mark.parametrize("q_len", [1, 40, 200])
-def test_cross_masked_rows_may_hold_anything(q_len, hd):
+@pytest.mark.parametrize("large", [False, True])
+def test_cross_masked_rows_may_hold_anything(large, q_len, hd):
     """Masked keys and values (and rows behind the last request) with infinities
     and NaN; a request whose mask leaves nothing; whole blocks masked first."""
     k_lens = [300, 64, 129, 400]
     m = (np.random.default_rng(1).random(sum(k_lens)) < 0.5).astype(np.uint8)
     m[300:364] = 0
     m[493:493 + 260] = 0
-    Cross(4, 2, hd, "bf16", [q_len] * 4, k_lens, m).check(bad_masked=True)
+    Cross(4, 2, hd, "bf16", [q_len] * 4, k_lens, m, large=large).check(bad_masked=True)
 
 
 @pytest.mark.parametrize("hd", [32, 64, 128])
 @pytest.mark.parametrize("q_len", [1, 150])
 @pytest.mark.parametrize("k_len,at", [(300, 290), (9000, 4321)])
-def test_cross_keys_that_are_read_do_reach_the_result(k_len, at, q_len, hd):
+@pytest.mark.parametrize("large", [False, True])
+def test_cross_keys_that_are_read_do_reach_the_result(large, k_len, at, q_len, hd):
     """NaN and infinity in a key that counts spoil every query of its request and
     key head, NaN in a query that query's head, and nothing else."""
     for bad in (float("nan"), float("inf")):
-        c = Cross(4, 2, hd, "bf16", [q_len, q_len], [k_len, 200])
+        c = Cross(4, 2, hd, "bf16", [q_len, q_len], [k_len, 200], large=large)
         c.kv[at, 0] = bad           # key head 0: query heads 0 and 1 of the first request
         c.kv[k_len + 3, hd] = 0.0
         if bad != bad:
@@ -416,18 +435,19 @@ def test_cross_keys_that_are_read_do_reach_the_result(k_len, at, q_len, hd):
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("q_len", [1, 3, 70])
 @pytest.mark.parametrize("mask", [None, "random"])
-def test_cross_split_keys(mask, q_len, hd):
-    Cross(4, 2, hd, "bf16", [q_len, 1, q_len], [5000, 13, 9001], mask).check()
+@pytest.mark.parametrize("large", [False, True])
+def test_cross_split_keys(large, mask, q_len, hd):
+    Cross(4, 2, hd, "bf16", [q_len, 1, q_len], [5000, 13, 9001], mask, large=large).check()
 
 
 @pytest.mark.parametrize("qk_scale", [1e-3, 8.0])
 def test_cross_flat_and_sharp_softmax(qk_scale):
     """Nearly equal weights, and weights that all but select one key (a row
     maximum that keeps rising along the keys)."""
-    for hd, q in ((64, 130), (128, 1), (128, 140)):
-        c = Cross(2, 1, hd, "f16", [q], [900], qk_scale=qk_scale)
+    for hd, q, large in ((64, 130, False), (64, 130, True), (128, 1, False), (128, 140, False), (128, 140, True)):
+        c = Cross(2, 1, hd, "f16", [q], [900], qk_scale=qk_scale, large=large)
         ramp = torch.linspace(0.1, 1.0, 900, device="cuda")[:, None]
-        c.kv[:, :hd] = (c.kv[:, :hd].float() * ramp).half()
+        c.kv[:900, :hd] = (c.kv[:900, :hd].float() * ramp).half()
         c.check()
 
 
@@ -441,7 +461,8 @@ def test_cross_many_requests_with_splits_and_prompts():
     g = np.random.default_rng(4)
     q, k = g.integers(0, 2, 600), g.integers(0, 20, 600)
     q[77], k[77], q[300], k[300], q[599], k[599] = 1, 6000, 150, 90, 3, 7000
-    Cross(2, 1, 64, "bf16", q, k, "random").check()
+    for large in (False, True):
+        Cross(2, 1, 64, "bf16", q, k, "random", large=large).check()
 
 
 def test_cross_nothing_to_do():
@@ -463,7 +484,7 @@ def test_cross_mixed_offsets_as_lists_and_arrays():
     assert torch.equal(first, c.out)
 
 
-@pytest.mark.parametrize("q_lens,k_lens", [([1, 1], [5000, 40]), ([200, 1, 300], [4000, 700, 50])])
+@pytest.mark.parametrize("q_lens,k_lens", [([1, 1], [5000, 40]), ([200, 1, 300], [400, 70, 50]), ([600, 1, 900], [4000, 700, 50])])
 def test_cross_same_bits_every_time_and_when_captured(q_lens, k_lens):
     c = Cross(8, 2, 128, "bf16", q_lens, k_lens, "random")
     c.check()
@@ -491,7 +512,7 @@ def test_cross_same_bits_every_time_and_when_captured(q_lens, k_lens):
 
 def test_cross_two_streams_with_a_workspace_each():
     a = Cross(4, 1, 128, "bf16", [1], [9000], seed=1)
-    b = Cross(4, 1, 128, "bf16", [150], [3000], seed=2)
+    b = Cross(4, 1, 128, "bf16", [150], [3000], seed=2, large=True)
     a.check()
     b.check()
     wants = a.out.clone(), b.out.clone()
@@ -504,10 +525,10 @@ def test_cross_two_streams_with_a_workspace_each():
     assert torch.equal(wants[0], a.out) and torch.equal(wants[1], b.out)
 
 
-@pytest.mark.parametrize("q_len", [1, 160])
+@pytest.mark.parametrize("q_len", [1, 160, 16000])
 def test_cross_rows_beyond_32_bit_offsets(q_len):
     """Key rows so far apart that element offsets pass 2^32."""
-    hd, nk, ld = 64, 200, 24_000_000
+    hd, nk, ld = 64, 700, 7_000_000
     buf = torch.zeros(nk * ld, dtype=torch.bfloat16, device="cuda")
     rows = buf.view(nk, ld)
     rows[:, :2 * hd] = _draw((nk, 2 * hd), "bf16", 3)
