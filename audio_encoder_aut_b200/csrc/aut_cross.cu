@@ -543,17 +543,18 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
 }
 
 // The requests as kernel `list` (or the join) sees them: those with items, in
-// order, for the tile kernel those with long splits first (its blocks end together
+// order, for the kernels those with long splits first (their blocks end together
 // only if the last ones are short).  Returns how many.
 int fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int heads_kv, int hd,
               const int32_t *cu_q, const int32_t *cu_k, int n_seq) {
-    constexpr int kBuckets = 64;  // of key tiles, the last for all longer splits
+    constexpr int kBuckets = 64;  // of steps of keys, the first for all longer splits
     const int group = heads_q / heads_kv;
     int64_t items = 0, part = 0;
     int n = 0, first[kBuckets + 1] = {0};
     const auto bucket = [&](int keys) {
-        const int tiles = (int)(((int64_t)keys + kCrossTileKeys - 1) / kCrossTileKeys);
-        return kBuckets - 1 - std::min(tiles, kBuckets - 1);
+        const int unit = kUnit[list];
+        const int steps = (int)(((int64_t)keys + unit - 1) / unit);
+        return kBuckets - 1 - std::min(steps, kBuckets - 1);
     };
     const auto visit = [&](auto &&use) {
         part = 0;
@@ -567,7 +568,7 @@ int fill_seqs(CrossSeq *out, int list, const CrossPlan &p, int heads_q, int head
             if (s.n > 1) part += (int64_t)nq * heads_q * s.n;
         }
     };
-    if (list == kTilesKernel) {
+    if (list != kJoin) {
         visit([&](const CrossSeq &s) { ++first[bucket(s.keys) + 1]; });
         for (int b = 0; b < kBuckets; ++b) first[b + 1] += first[b];
         n = first[kBuckets];
