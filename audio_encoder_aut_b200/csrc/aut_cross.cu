@@ -9,7 +9,8 @@
 // keys with the running maximum and sum of the softmax.
 //
 // cross_rows_kernel: 16 rows (query, head of the group) of one request and key
-// head per block.  With so few rows the work is reading keys and values once, so
+// head per block.  With so few rows the work is reading keys and values once (256
+// requests of one token on 780 keys, 16 heads of 128 over 8: 122 us, 6.7 TB/s), so
 // the block's four warps each stream key blocks of their own (block w, w + 4, ...)
 // through a private ring of cp.async copies, with no barrier between warps until
 // their results are joined at the end.  A masked key, or one past the end, is
@@ -39,7 +40,7 @@ namespace {
 
 // Small rings, so that three blocks share a SM: most requests of a batch are a step
 // or two long, and a block's start and end are then most of its time (256 requests
-// of 6 to 780 keys: 36.5 us; 65 us with 32 keys and 3 stages, one block a SM).
+// of 6 to 780 keys: 38 us; 65 us with 32 keys and 3 stages, one block a SM).
 constexpr int kRows = 16;    // rows of one block
 constexpr int kRowWarps = 4;
 constexpr int kKeys = 16;    // keys of a warp's block (at most a lane each, for the mask)
@@ -403,12 +404,11 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
 // The kernels a request may run on, and the join after them.
 enum { kRowsKernel = 0, kTilesKernel = 1, kJoin = 2, kLists = 3 };
 
-// Blocks the splits of one kernel aim for (three a SM, or one), the fewest keys
-// worth a split of their own, and the keys a split is rounded to (whole steps of
-// the row kernel's four warps; whole tiles).  One token on 15600 keys, 8 key heads
-// of 128: 14.8 us with these, 17.2 us with splits of 512, 22.5 us with one block
-// a SM.
-constexpr int kTargetItems[2] = {3 * 148, 148};
+// Blocks that the row kernel's splits aim for (three a SM); the fewest keys worth a
+// split of their own; and the keys a split is rounded to (whole steps of the row
+// kernel's four warps; whole tiles).  One token on 15600 keys, 8 key heads of 128:
+// 14.8 us with these, 17.2 us with splits of 512, 22.5 us with one block a SM.
+constexpr int kRowsTarget = 3 * 148;
 constexpr int kMinChunk[2] = {256, 512};
 constexpr int kUnit[2] = {kRowWarps * kKeys, kCrossTileKeys};
 
@@ -475,6 +475,52 @@ int64_t split_items(int kernel, int64_t nq, int group, int heads_kv) {
     return (nq * group + rows - 1) / rows * heads_kv;
 }
 
+// The tile kernel's chunk.  Its items run one a SM, so a few more than a whole
+// number of waves cost a wave, and a split pays only if it fills the last one:
+// of a few candidates, the one with the least estimated time.  An item takes 3.5 us
+// and 2.05 us a tile of keys (1.95 with head_dim 64), a join 2 us and the partial
+// rows' way to memory and back.  (16 heads of 128 over 8, 512 x 4096: 4 requests
+// take 70 us whole and 90 us in the halves that an even share of the work would
+// ask for, one request 69 us whole.)
+int tile_chunk(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
+               int n_seq, CrossPlan p) {
+    const int group = heads_q / heads_kv, unit = kUnit[kTilesKernel];
+    int longest = 0;
+    for (int i = 0; i < n_seq; ++i)
+        if (kernel_of(cu_q[i + 1] - cu_q[i], group, hd, p) == kTilesKernel)
+            longest = std::max(longest, cu_k[i + 1] - cu_k[i]);
+    const int whole = std::max(longest, 1);
+    double best = 0;
+    int best_chunk = whole;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48}) {
+        p.chunk[kTilesKernel] = (int)(((int64_t)whole / s + unit) / unit * unit);
+        if (s > 1 && p.chunk[kTilesKernel] < kMinChunk[kTilesKernel]) break;
+        double items = 0, sum = 0, most = 0, least = 1e30, joined = 0;
+        for (int i = 0; i < n_seq; ++i) {
+            const int64_t nq = cu_q[i + 1] - cu_q[i];
+            if (nq == 0 || kernel_of(nq, group, hd, p) != kTilesKernel) continue;
+            const Splits sp = split_keys(cu_k[i + 1] - cu_k[i], kTilesKernel, p);
+            const double n = (double)split_items(kTilesKernel, nq, group, heads_kv) * sp.n;
+            const double us = 3.5 + (hd > 64 ? 2.05 : 1.95) * (((int64_t)sp.keys + unit - 1) / unit);
+            items += n;
+            sum += n * us;
+            most = std::max(most, us);
+            least = std::min(least, us);
+            if (sp.n > 1) joined += (double)nq * heads_q * sp.n;
+        }
+        if (items == 0) break;
+        const double waves = items / 148;
+        const double us = std::max(most, sum / 148 + (std::ceil(waves) - waves) * least) +
+                          (joined > 0 ? 2.0 + joined * hd * 2e-6 : 0.0);
+        if (s == 1 || us < best) {
+            best = us;
+            best_chunk = p.chunk[kTilesKernel];
+        }
+        if (waves > 4) break;  // the last wave is a small part of the whole
+    }
+    return best_chunk;
+}
+
 // Whether the row kernel would end a call's requests of more than one row block
 // before the tile kernel does.  Estimates in us from what both measured over 20 to 512 rows, 100
 // to 4000 keys, 1 and 16 requests: the row kernel takes 3.3 (4.3 with head_dim
@@ -499,7 +545,7 @@ bool small_call(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const in
     const bool wide = hd > 64;
     const double share = tiles / 148, whole = (double)kMinChunk[kTilesKernel] / kCrossTileKeys;
     const double rows_us =
-        (wide ? 4.3 : 3.3) + (wide ? 0.032 : 0.019) * block_keys / kTargetItems[kRowsKernel];
+        (wide ? 4.3 : 3.3) + (wide ? 0.032 : 0.019) * block_keys / kRowsTarget;
     const double tiles_us = (wide ? 7.0 : 5.2) * std::max(1.0, items / 148) +
                             (wide ? 2.0 : 1.45) * std::max(share, std::min(most, whole)) +
                             (most > whole ? 2.0 : 0.0);
@@ -512,18 +558,17 @@ aut_status plan_cross(int heads_q, int heads_kv, int hd, const int32_t *cu_q, co
     p->small_call = small_call(heads_q, heads_kv, hd, cu_q, cu_k, n_seq);
     for (int i = 0; i < n_seq; ++i)
         p->long_prompts |= (int64_t)(cu_q[i + 1] - cu_q[i]) * group > 2 * kRows;
-    int64_t work[2] = {0, 0};  // keys read by all of a kernel's items, unsplit
+    int64_t work = 0;  // keys read by all of the row kernel's items, unsplit
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i];
-        const int kernel = kernel_of(nq, group, hd, *p);
-        work[kernel] += split_items(kernel, nq, group, heads_kv) * (cu_k[i + 1] - cu_k[i]);
+        if (kernel_of(nq, group, hd, *p) == kRowsKernel)
+            work += split_items(kRowsKernel, nq, group, heads_kv) * (cu_k[i + 1] - cu_k[i]);
     }
     // Every split about as long as one block's share of the whole.
-    for (int kernel = 0; kernel < 2; ++kernel) {
-        const int64_t share = (work[kernel] + kTargetItems[kernel] - 1) / kTargetItems[kernel];
-        p->chunk[kernel] = (int)std::min<int64_t>(std::max<int64_t>(share, kMinChunk[kernel]), 1 << 30);
-        p->chunk[kernel] = (p->chunk[kernel] + kUnit[kernel] - 1) / kUnit[kernel] * kUnit[kernel];
-    }
+    const int64_t share = std::min<int64_t>((work + kRowsTarget - 1) / kRowsTarget, 1 << 30);
+    const int unit = kUnit[kRowsKernel];
+    p->chunk[kRowsKernel] = std::max(((int)share + unit - 1) / unit * unit, kMinChunk[kRowsKernel]);
+    p->chunk[kTilesKernel] = tile_chunk(heads_q, heads_kv, hd, cu_q, cu_k, n_seq, *p);
     for (int i = 0; i < n_seq; ++i) {
         const int64_t nq = cu_q[i + 1] - cu_q[i], nk = cu_k[i + 1] - cu_k[i];
         if (nq == 0) continue;

@@ -14,16 +14,24 @@
 //              out
 //   warp 8     TMA producer: K and V tiles (128 keys, 128-byte swizzle) in
 //              turn through a ring of slots, each read by both row tiles
-//   warp 9     TMEM allocation; one thread issues the products.  P is the A
-//              operand from tensor memory
+//   warp 9     TMEM allocation, and the products.  P is the A operand from tensor
+//              memory
 // The one issuer alternates between the row tiles, so that while one tile's
 // softmax runs the other's products do.  (As two blocks a SM with one tile each,
 // the two issuers' products share the tensor pipe instruction by instruction, and
 // both blocks fall into step: softmax against softmax, products against products,
-// 528 us where the alternating issuer takes @ALT@ for 16 x 512 x 4096, 16 heads of
-// 128.)  With head_dim 64 the P columns fit beside S, and the next tile's S is
+// 528 us where the alternating issuer, otherwise the same, took 386 us for 16
+// requests of 512 x 4096, 16 heads of 128.)  With head_dim 64 the P columns fit beside S, and the next tile's S is
 // computed while this tile's softmax runs; with 128 P takes the place of the S
 // it came from, and the next S follows P V in the tensor pipe's order.
+//
+// Bound by the chain S -> softmax -> P V -> S of a row tile, of which the tensor
+// cores are busy 45%: 16 requests of 512 x 4096, 16 heads of 128: 273 us, 1006
+// TFLOP/s, 0.61 of the measured bf16 peak; head_dim 64 (32 heads) 450 us, 611 TFLOP/s, where the
+// exponentials of both row tiles take their pipe's whole time.  Tried without gain:
+// a part of the exponentials as a polynomial on the FMA pipe (issue slots run out
+// instead), two threads a row (registers spill), P V of a tile's first 96 keys
+// before the rest's P is made, and persistent blocks (the loop's registers).
 //
 // Keys past the request's end or masked out score -inf, and their V rows are
 // zeroed in shared memory (they may hold anything, and 0 * NaN is NaN).

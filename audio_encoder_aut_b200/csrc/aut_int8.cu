@@ -19,7 +19,8 @@ namespace {
 // long for them is read a second time).  Bound by HBM, one read
 // of x and one write of q, as long as an element costs no more than about ten
 // instructions and none on the conversion pipe: the maximum is taken on the bits,
-// two 16-bit elements at a time, and rounding is an addition.
+// two 16-bit elements at a time, and rounding is an addition.  15600 x 5120: 59 us
+// from bf16 (4.1 TB/s), 71 us from fp32 (5.6 TB/s).
 
 constexpr int kQuantThreads = 256;
 
@@ -166,7 +167,7 @@ cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, 
 // operand words of two products (the same permutation of K on both sides), so
 // weights and tokens go from global memory to registers in 16-byte loads with no
 // shared memory between.  The warps' int32 sums meet in shared memory: exact, so
-// in any order.
+// in any order.  One token, 2048 x 2048: 2.2 us, a launch's latency.
 
 constexpr int kFewThreads = 256;
 constexpr int kFewTokens = 32;
