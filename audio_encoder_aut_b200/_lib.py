@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from ctypes import (POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p)
 
 # AUT_LIB=debug selects the bounds-checked build (libaut_debug.so, built by
@@ -57,10 +58,14 @@ class aut_trace(ctypes.Structure):
                 ("kinds", POINTER(c_int32))]
 
 
-class aut_head_rows(ctypes.Structure):
-    _fields_ = [("x", c_void_p), ("ld_x", c_int64), ("y", c_void_p), ("ld_y", c_int64),
-                ("gamma", c_void_p), ("positions", c_void_p), ("rows", c_int32),
-                ("heads", c_int32)]
+_HEAD_ROWS = struct.Struct("@PqPqPPii")
+
+
+def aut_head_rows(x: int, ld_x: int, y: int, ld_y: int, gamma: int | None, positions: int | None,
+                  rows: int, heads: int) -> bytes:
+    """An aut_head_rows struct for aut_qk_norm_rope, as its bytes (a ctypes Structure takes
+    longer to fill and to pass than the kernel takes for one token)."""
+    return _HEAD_ROWS.pack(x or 0, ld_x, y or 0, ld_y, gamma or 0, positions or 0, rows, heads)
 
 
 class AutError(RuntimeError):
@@ -112,9 +117,8 @@ _SIGNATURES = {
     "aut_linear_i8": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                 c_int32, c_int32, c_int32, c_int32, c_void_p, c_int32, c_int32,
                                 c_void_p]),
-    "aut_qk_norm_rope": (c_int32, [POINTER(aut_head_rows), POINTER(aut_head_rows), c_int32,
-                                   c_int32, c_int32, c_int32, c_double, c_int32, c_float,
-                                   c_void_p]),
+    "aut_qk_norm_rope": (c_int32, [c_char_p, c_char_p, c_int32, c_int32, c_int32, c_int32,
+                                   c_double, c_int32, c_float, c_void_p]),
     "aut_cross_attention": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
                                       c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
                                       c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p,
@@ -325,12 +329,12 @@ def aut_linear_i8(xq: int, x_scale: int, wq: int, w_scale: int, bias: int | None
                                timeout_ms, flags, stream)
 
 
-def aut_qk_norm_rope(q: aut_head_rows | None, k: aut_head_rows | None, head_dim: int,
-                     x_dtype: int, y_dtype: int, rot_dim: int, theta: float, interleaved: bool,
-                     eps: float, stream: int) -> int:
-    return lib().aut_qk_norm_rope(ctypes.byref(q) if q is not None else None,
-                                  ctypes.byref(k) if k is not None else None, head_dim, x_dtype,
-                                  y_dtype, rot_dim, theta, int(interleaved), eps, stream)
+def aut_qk_norm_rope(q: bytes | None, k: bytes | None, head_dim: int, x_dtype: int, y_dtype: int,
+                     rot_dim: int, theta: float, interleaved: bool, eps: float,
+                     stream: int) -> int:
+    """q and k: from aut_head_rows, or None."""
+    return lib().aut_qk_norm_rope(q, k, head_dim, x_dtype, y_dtype, rot_dim, theta, interleaved,
+                                  eps, stream)
 
 
 def aut_cross_attention(q: int, ld_q: int, k: int, ld_k: int, v: int, ld_v: int, out: int,

@@ -14,7 +14,7 @@ namespace aut {
 namespace {
 
 // ---------------------------------------------------------------- quantise --
-// scale = max |x| / 127, q = rint(x / scale): the row's maximum first, then the
+// scale = max |x| (1 / 127), q = rint(x / scale): the row's maximum first, then the
 // row again, so a row is kept in registers between the two (the rest of a row too
 // long for them is read a second time).  Bound by HBM, one read
 // of x and one write of q, as long as an element costs no more than about ten
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_k
     }
     const float amax = bits_value<T>(top);
     const bool finite = amax < INFINITY;
-    const float s = finite ? amax / 127.f : amax;
+    const float s = finite ? amax * (1.f / 127.f) : amax;
     if (t == 0) scale[row] = s;
     const bool zero = !finite || s == 0.f;
     const float inv = 1.f / s;

@@ -338,8 +338,8 @@ size_t aut_inject_workspace_bytes(int32_t L);
 typedef enum { AUT_BF16 = 0, AUT_F16 = 1, AUT_F32 = 2 } aut_dtype;
 
 /* No passage: a library operator.  Rows to 8-bit integers with a scale each:
- * scale[m] = max_k |x[m, k]| / 127 and q[m, k] = x[m, k] / scale[m] rounded to
- * nearest even, both in fp32 (IEEE division), so x ~ scale[m] q[m, k].  A row
+ * scale[m] = max_k |x[m, k]| * (1 / 127) and q[m, k] = x[m, k] / scale[m] rounded to
+ * nearest even, both in fp32 (IEEE product and division), so x ~ scale[m] q[m, k].  A row
  * of zeros gets scale 0 and zeros; a row that holds an infinity or NaN gets
  * that as its scale and zeros, which aut_linear_i8 turns into a row of NaN.
  * x: device, `dtype` (aut_dtype) [M, K] with row stride ld_x >= K, rows 16-byte

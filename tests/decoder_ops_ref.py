@@ -14,7 +14,7 @@ def quantize(x):
     x = np.asarray(x, np.float32)
     amax = np.abs(x).max(1)
     with np.errstate(all="ignore"):
-        scale = np.where(np.isfinite(amax), (amax / np.float32(127)).astype(np.float32), amax)
+        scale = np.where(np.isfinite(amax), amax * (np.float32(1) / np.float32(127)), amax)
         s = np.where((scale > 0) & np.isfinite(scale), scale, np.float32(1))
         q = np.clip(np.rint((x / s[:, None]).astype(np.float32)), -127, 127)
     q[~(np.isfinite(scale) & (scale > 0))] = 0

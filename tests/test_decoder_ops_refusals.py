@@ -38,8 +38,7 @@ def test_linear_i8_few_rows_has_no_wait_to_inject_into():
 
 
 def _rows(**over):
-    arg = dict(x=P, ld_x=128, y=P, ld_y=128, gamma=P, positions=P, rows=3, heads=2) | over
-    return A.aut_head_rows(*[arg[n] for n, _ in A.aut_head_rows._fields_])
+    return A.aut_head_rows(**(dict(x=P, ld_x=128, y=P, ld_y=128, gamma=P, positions=P, rows=3, heads=2) | over))
 
 
 @pytest.mark.parametrize("over,want", [
