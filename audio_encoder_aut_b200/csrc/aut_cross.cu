@@ -114,11 +114,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 join_ml[kRowWarps][kRows];
     pdl_trigger();
-    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // The item: from the parameters, if the list is there, while the previous
+    // kernel ends.
+    if (a.seqs) pdl_wait();
     const CrossSeq *seqs = a.seqs ? a.seqs : a.inline_seqs;
-    const int seq = cross_find(seqs, a.n_seq, blockIdx.x, lane);
-    const CrossSeq s = seqs[seq];
+    const CrossSeq s = seqs[cross_find(seqs, a.n_seq, blockIdx.x, lane)];
     const int nq = s.nq, rows = nq * a.group, tiles = (rows + kRows - 1) / kRows;
     int item = (int)blockIdx.x - s.item;
     const int tile = item % tiles;
@@ -126,6 +127,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     const int hk = item % a.heads_kv, split = item / a.heads_kv;
     const int key0 = s.k0 + split * s.keys, key1 = min(s.k0 + s.nk, key0 + s.keys);
     const int n_blocks = (key1 - key0 + kKeys - 1) / kKeys;  // 0 for a request without keys
+
+    pdl_wait();
 
     // Row r of the tile: query (tile 16 + r) / group, head hk group + (tile 16 + r) % group.
     auto row_at = [&](int r, int &tok, int &head) {
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
     __shared__ float4 team_v[kTeams][kLanes][2];
     __shared__ float2 team_ml[kTeams];
     pdl_trigger();
-    pdl_wait();
+    if (a.seqs) pdl_wait();
     const int lane = threadIdx.x & 31, team = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
     const int groups = a.join_groups, g = team % groups;
     const int first = (int)blockIdx.x * (kTeams / groups), item = first + team / groups;
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
     const int r = item - s.item, tok = r / a.heads_q, head = r - tok * a.heads_q;
     const int splits = in ? s.splits : 0;
     const size_t step = (size_t)s.nq * a.heads_q, row0 = (size_t)s.part + r;
+    pdl_wait();
     float mx = -INFINITY, sum = 0.f, v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -642,7 +646,7 @@ CrossLayout cross_layout(const CrossPlan &p, int hd, int n_seq) {
         off += (bytes + 255) / 256 * 256;
         return o;
     };
-    const size_t list = n_seq > kCrossInline ? (size_t)(n_seq + 1) * sizeof(CrossSeq) : 0;
+    const size_t list = n_seq > kCrossInline ? ((size_t)n_seq + 1) * sizeof(CrossSeq) : 0;
     for (size_t &at : l.list) at = take(list);
     l.part_o = take((size_t)p.part_rows * hd * 4);
     l.part_ml = take((size_t)p.part_rows * 8);
@@ -740,7 +744,7 @@ extern "C" aut_status aut_cross_attention(
     a.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + lay.part_ml);
     const bool listed = n_seq > kCrossInline;
-    CrossSeq *list = listed ? new (std::nothrow) CrossSeq[n_seq + 1] : a.inline_seqs;
+    CrossSeq *list = listed ? new (std::nothrow) CrossSeq[(size_t)n_seq + 1] : a.inline_seqs;
     if (!list) return AUT_ERR_WORKSPACE;
     aut_status result = AUT_OK;
     for (int i = 0; i < kLists && result == AUT_OK; ++i) {
@@ -752,7 +756,7 @@ extern "C" aut_status aut_cross_attention(
         if (listed) {
             CrossSeq *dev = reinterpret_cast<CrossSeq *>(ws + lay.list[i]);
             a.seqs = dev;
-            if (launch_upload(reinterpret_cast<const int32_t *>(list), (size_t)(a.n_seq + 1) * (sizeof(CrossSeq) / 4),
+            if (launch_upload(reinterpret_cast<const int32_t *>(list), ((size_t)a.n_seq + 1) * (sizeof(CrossSeq) / 4),
                               reinterpret_cast<int32_t *>(dev), s) != cudaSuccess)
                 result = AUT_ERR_CUDA;
         }

@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kFewThreads) linear_i8_few_kernel(
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int kMaxK8 = 131072;  // 127^2 * 131072 < 2^31
+constexpr int kMaxK8 = 131072;         // 127^2 * 131072 < 2^31
+constexpr int kMaxRows = 0x7ffff000;   // row indexes are 32-bit, a block's spare rows included
 
 }  // namespace
 }  // namespace aut
@@ -263,7 +264,7 @@ using namespace aut;
 extern "C" aut_status aut_quantize_rows(const void *x, int32_t dtype, int64_t ld_x, int32_t M,
                                         int32_t K, void *q, void *scale, aut_stream_t stream) {
     if (dtype < AUT_BF16 || dtype > AUT_F32 || M < 0 || K <= 0) return AUT_ERR_INVALID_ARG;
-    if (K % 16 || K > kMaxK8) return AUT_ERR_UNSUPPORTED;
+    if (K % 16 || K > kMaxK8 || M > kMaxRows) return AUT_ERR_UNSUPPORTED;
     if (M == 0) return AUT_OK;
     const int64_t es = dtype == AUT_F32 ? 4 : 2;
     if (!x || !q || !scale || ld_x < K || (ld_x * es) % 16 || ld_x > (int64_t)1 << 40)
@@ -287,7 +288,7 @@ extern "C" aut_status aut_linear_i8(const void *xq, const void *x_scale, const v
     if (M < 0 || N <= 0 || K <= 0 || epilogue < 0 || epilogue > 3 || timeout_ms < 0)
         return AUT_ERR_INVALID_ARG;
     if (flags & ~(AUT_LINEAR_FAULT_INJECT | AUT_LINEAR_SINGLE_CTA)) return AUT_ERR_INVALID_ARG;
-    if (K % 16 || N % 16 || K > kMaxK8) return AUT_ERR_UNSUPPORTED;
+    if (K % 16 || N % 16 || K > kMaxK8 || M > kMaxRows) return AUT_ERR_UNSUPPORTED;
     if (M == 0) return AUT_OK;
     if (!xq || !x_scale || !wq || !w_scale || !y) return AUT_ERR_INVALID_ARG;
     if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(w_scale, 16) || !aligned(y, 16) ||

@@ -13,7 +13,7 @@ BAD, UNS, WS = A.AUT_ERR_INVALID_ARG, A.AUT_ERR_UNSUPPORTED, A.AUT_ERR_WORKSPACE
 
 @pytest.mark.parametrize("over,want", [
     (dict(dtype=3), BAD), (dict(dtype=-1), BAD), (dict(M=-1), BAD), (dict(K=0), BAD), (dict(K=24), UNS), (dict(K=131088), UNS),
-    (dict(x=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD), (dict(x=P + 8), BAD), (dict(q=P + 8), BAD),
+    (dict(M=(1 << 31) - 1), UNS), (dict(x=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD), (dict(x=P + 8), BAD), (dict(q=P + 8), BAD),
     (dict(scale=P + 2), BAD), (dict(ld_x=48), BAD), (dict(ld_x=68), BAD), (dict(ld_x=1 << 41), BAD), (dict(M=0, x=None), A.AUT_OK)])
 def test_quantize_rows_refuses(over, want):
     arg = dict(x=P, dtype=A.BF16, ld_x=64, M=4, K=64, q=P, scale=P, stream=0) | over
@@ -22,7 +22,7 @@ def test_quantize_rows_refuses(over, want):
 
 @pytest.mark.parametrize("M", [4, 400])
 @pytest.mark.parametrize("over,want", [
-    (dict(N=24), UNS), (dict(K=40), UNS), (dict(K=131088), UNS), (dict(N=0), BAD), (dict(K=-16), BAD), (dict(epilogue=4), BAD),
+    (dict(N=24), UNS), (dict(K=40), UNS), (dict(K=131088), UNS), (dict(M=(1 << 31) - 1), UNS), (dict(N=0), BAD), (dict(K=-16), BAD), (dict(epilogue=4), BAD),
     (dict(epilogue=-1), BAD), (dict(timeout_ms=-1), BAD), (dict(flags=A.LINEAR_F16), BAD), (dict(flags=8), BAD), (dict(xq=None), BAD),
     (dict(x_scale=None), BAD), (dict(wq=None), BAD), (dict(w_scale=None), BAD), (dict(y=None), BAD), (dict(xq=P + 8), BAD),
     (dict(wq=P + 4), BAD), (dict(w_scale=P + 4), BAD), (dict(x_scale=P + 1), BAD), (dict(bias=P + 2), BAD), (dict(y=P + 8), BAD)])
