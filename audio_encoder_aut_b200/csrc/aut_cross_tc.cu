@@ -342,15 +342,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------- softmax --
         // Q into shared memory.
+        if (n > 0) {
+            // Not for a request without keys: nothing would order these writes before
+            // the output's, which goes out through the same place.
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            const int i = threadIdx.x + u * 32 * kSoftmaxWarps, r = i / kChunks, c = i % kChunks;
-            *reinterpret_cast<uint4 *>(sm + (r >> 7) * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
-                                       (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = qv[u];
+            for (int u = 0; u < kLoads; ++u) {
+                const int i = threadIdx.x + u * 32 * kSoftmaxWarps, r = i / kChunks, c = i % kChunks;
+                *reinterpret_cast<uint4 *>(sm + (r >> 7) * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
+                                           (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = qv[u];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
 
         const int rt = warp >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;  // of the row tile, and TMEM lane

@@ -471,6 +471,20 @@ def test_cross_nothing_to_do():
     Cross(2, 1, 64, "bf16", [2, 0], [0, 0]).check()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_cross_requests_without_keys_among_prompts(hd):
+    """Zeros for the rows of requests without keys, call after call: nothing else of
+    such a block may reach its output."""
+    c = Cross(16, 8, hd, "bf16", [29, 300, 200, 64, 17, 128], [0, 0, 5, 0, 0, 0], large=True)
+    c.check()
+    first = c.out.clone()
+    for _ in range(200):
+        c.out.fill_(7)
+        assert c.call() == A.AUT_OK
+        assert torch.equal(c.out, first)
+    assert not first[:329].any() and not first[529:738].any()
+
+
 def test_cross_mixed_offsets_as_lists_and_arrays():
     c = Cross(4, 2, 64, "bf16", [1, 20], [50, 60])
     assert c.call() == A.AUT_OK
