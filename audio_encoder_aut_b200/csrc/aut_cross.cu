@@ -11,7 +11,7 @@
 // cross_rows_kernel: 16 rows (query, head of the group) of one request and key
 // head per block.  With so few rows the work is reading keys and values once (256
 // requests of one token on 780 keys, 16 heads of 128 over 8: 122 us, 6.7 TB/s), so
-// the block's four warps each stream key blocks of their own (block w, w + 4, ...)
+// the block's warps each stream key blocks of their own (block w, w + W, ...)
 // through a private ring of cp.async copies, with no barrier between warps until
 // their results are joined at the end.  A masked key, or one past the end, is
 // zero-filled by its copy: whatever stands there never enters.  Scores and P V
@@ -43,16 +43,20 @@ namespace {
 // of 6 to 780 keys: 38 us; 65 us with 32 keys and 3 stages, one block a SM).
 constexpr int kRows = 16;    // rows of one block
 constexpr int kRowWarps = 4;
+// With no more blocks than SMs there is room for twice the warps, and half the
+// steps (one token, 16 heads of 128: 6.6 us against 9.2 us on 2000 keys; on a full GPU
+// they cost, 65 us against 37 us for 256 requests).
+constexpr int kRowWarpsAlone = 8;
 constexpr int kKeys = 16;    // keys of a warp's block (at most a lane each, for the mask)
 constexpr int kStages = 2;   // blocks a warp holds in its ring
 
-template <int HD>
+template <int HD, int W>
 struct RowsCfg {
     static constexpr int kRowBytes = HD * 2;
     static constexpr int kTile = kKeys * kRowBytes;  // K or V of one block
     static constexpr int kWarpBytes = kStages * 2 * kTile;
-    static constexpr int kJoin = kRowWarps * kRows * (HD + 4) * 4;  // the warps' O, padded rows
-    static constexpr int kSmem = kRowWarps * kWarpBytes > kJoin ? kRowWarps * kWarpBytes : kJoin;
+    static constexpr int kJoin = W * kRows * (HD + 4) * 4;  // the warps' O, padded rows
+    static constexpr int kSmem = W * kWarpBytes > kJoin ? W * kWarpBytes : kJoin;
 };
 
 // Byte offset of the 16-byte chunk c of row r of a K or V block; the chunks of
@@ -107,12 +111,12 @@ AUT_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kRowWarps * 32, 3)
+template <typename T, int HD, int W>
+__global__ void __launch_bounds__(W * 32, W == kRowWarps ? 3 : 1)
     cross_rows_kernel(const __grid_constant__ CrossArgs a) {
-    using Cfg = RowsCfg<HD>;
+    using Cfg = RowsCfg<HD, W>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 join_ml[kRowWarps][kRows];
+    __shared__ float2 join_ml[W][kRows];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // The item: from the parameters, if the list is there, while the previous
@@ -166,10 +170,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     uint32_t keys[kStages];  // of the blocks in the ring
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        keys[i] = block_keys(warp + i * kRowWarps);
-        copy_block(warp + i * kRowWarps, keys[i], i);
+        keys[i] = block_keys(warp + i * W);
+        copy_block(warp + i * W, keys[i], i);
     }
-    uint32_t ahead = block_keys(warp + (kStages - 1) * kRowWarps);
+    uint32_t ahead = block_keys(warp + (kStages - 1) * W);
     // Queries as product operands: rows g and g + 8, columns 16 c + 2 t (+ 8).
     uint32_t qf[HD / 16][4];
 #pragma unroll
@@ -191,14 +195,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8; l: this lane's share
 
     int stage = 0;
-    for (int b = warp; b < n_blocks; b += kRowWarps) {
+    for (int b = warp; b < n_blocks; b += W) {
         {  // the block kStages - 1 ahead, into the stage the previous step has read
             const int fill = stage == 0 ? kStages - 1 : stage - 1;
 #pragma unroll
             for (int i = 0; i < kStages; ++i)
                 if (i == fill) keys[i] = ahead;
-            copy_block(b + (kStages - 1) * kRowWarps, ahead, fill);
-            ahead = block_keys(b + kStages * kRowWarps);
+            copy_block(b + (kStages - 1) * W, ahead, fill);
+            ahead = block_keys(b + kStages * W);
         }
         copy_wait<kStages - 1>();
         __syncwarp();
@@ -293,19 +297,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3)
                 make_float2(o[c][2 * i], o[c][2 * i + 1]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * (HD / 8); i += kRowWarps * 32) {
+    for (int i = threadIdx.x; i < kRows * (HD / 8); i += W * 32) {
         const int r = i / (HD / 8), c = i % (HD / 8);
         int tok, head;
         if (!row_at(r, tok, head)) continue;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, join_ml[w][r].x);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, join_ml[w][r].x);
         const float base = mx == -INFINITY ? 0.f : mx;
         float sum = 0.f, v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = ex2_approx(join_ml[w][r].x - base);
             sum = fmaf(f, join_ml[w][r].y, sum);
 #pragma unroll
@@ -530,7 +534,7 @@ int tile_chunk(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int
 // to 4000 keys, 1 and 16 requests: the row kernel takes 3.3 (4.3 with head_dim
 // 128) and 19 (32) ns for every key of a block, three blocks a SM; the tile kernel
 // 5.2 (7) an item and 1.45 (2) a tile of keys, one item a SM, and 2 for a join.
-// One request, 16 heads of 64, 128 rows: 5.4 against 11.8 us on 400 keys, 25
+// One request, 16 heads of 64, 128 rows: 4.9 against 11.8 us on 400 keys, 25
 // against 18 us on 4000.
 bool small_call(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
                 int n_seq) {
@@ -654,12 +658,17 @@ CrossLayout cross_layout(const CrossPlan &p, int hd, int n_seq) {
     return l;
 }
 
+template <typename T, int HD, int W>
+cudaError_t launch_rows(const CrossArgs &a, cudaStream_t st) {
+    constexpr int smem = RowsCfg<HD, W>::kSmem;
+    const cudaError_t e = smem_attr_once<cross_rows_kernel<T, HD, W>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cross_rows_kernel<T, HD, W>, dim3(a.items), dim3(W * 32), smem, st, 1, a);
+}
 template <typename T, int HD>
 cudaError_t launch_rows(const CrossArgs &a, cudaStream_t st) {
-    constexpr int smem = RowsCfg<HD>::kSmem;
-    const cudaError_t e = smem_attr_once<cross_rows_kernel<T, HD>>(smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(cross_rows_kernel<T, HD>, dim3(a.items), dim3(kRowWarps * 32), smem, st, 1, a);
+    return a.items <= sm_count_cached() ? launch_rows<T, HD, kRowWarpsAlone>(a, st)
+                                        : launch_rows<T, HD, kRowWarps>(a, st);
 }
 
 template <typename T, int HD>
