@@ -16,6 +16,7 @@
 //              turn through a ring of slots, each read by both row tiles
 //   warp 9     TMEM allocation, and the products.  P is the A operand from tensor
 //              memory
+//   warps 10, 11  zeros over the V rows of keys that are not read
 // The one issuer alternates between the row tiles, so that while one tile's
 // softmax runs the other's products do.  (As two blocks a SM with one tile each,
 // the two issuers' products share the tensor pipe instruction by instruction, and
@@ -52,7 +53,7 @@ namespace {
 
 constexpr int kM = 128, kN = kCrossTileKeys;  // rows of a tile, keys of a tile
 constexpr int kSoftmaxWarps = 8;              // four per row tile
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups; two warps idle
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups
 // Registers a thread: 168 at launch (three warps to a quarter of the register
 // file), of which the third warpgroup gives some to the softmax, whose rows of
 // 128 scores otherwise spill.  256 * 208 + 128 * 80 <= 384 * 168.
@@ -70,8 +71,11 @@ struct TcCfg {
     static constexpr uint32_t kColP = kEarlyS ? kColO + 2 * HD : 0;
     static constexpr uint32_t kStepP = kEarlyS ? kN / 2 : kN;  // from one row tile's P to the other's
     static constexpr int kOffBar = kTileBytes * (2 + kSlots);
-    // full, empty [kSlots]; q_full; s_full, s_read, p_full, pv_done [2]; mma_done
-    static constexpr int kBars = 2 * kSlots + 10;
+    // V tiles until one takes the same slot again.
+    static constexpr int kCleanRing = kSlots % 2 ? kSlots : kSlots / 2;
+    // full, empty [kSlots]; q_full; s_full, s_read, p_full, pv_done [2]; mma_done;
+    // loading, clean [kCleanRing]
+    static constexpr int kBars = 2 * kSlots + 10 + 2 * kCleanRing;
     static constexpr int kSmem = 1024 + kOffBar + kBars * 8 + 16;
     static_assert(kColO + 2 * HD + (kEarlyS ? kN : 0) <= kTmemCols, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory of a block");
@@ -147,7 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *p_full = s_read + 2;
     uint64_t *pv_done = p_full + 2;
     uint64_t *mma_done = pv_done + 2;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    // V tiles that may miss keys, one after the other: on their way, and ready.
+    uint64_t *loading = mma_done + 1;  // [kCleanRing]
+    uint64_t *clean = loading + Cfg::kCleanRing;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(clean + Cfg::kCleanRing);
     int *abort_flag = reinterpret_cast<int *>(tslot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_v = abort_flag;
@@ -170,6 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(pv_done + i, 1);
         }
         mbar_init(mma_done, 1);
+        for (int i = 0; i < Cfg::kCleanRing; ++i) {
+            mbar_init(loading + i, 1);
+            mbar_init(clean + i, 2);
+        }
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
@@ -190,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key0 = s.k0 + split * s.keys, key1 = min(s.k0 + s.nk, key0 + s.keys);
     const int n = (key1 - key0 + kN - 1) / kN;  // key tiles; 0 for a request without keys
     const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
+    const int n_whole = a.mask ? 0 : max(0, key1 - key0) / kN;  // key tiles known to miss no key
 
             // Q: 16 bytes a thread, rows one after the other; the loads run while the block
     // sets itself up.
@@ -242,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < HD / 64; ++c)
                     tma_load_2d(slots + i * Cfg::kTileBytes + c * Cfg::kAtom, t & 1 ? &tm_v : &tm_k,
                                 full + i, hk * HD + 64 * c, key0 + (t >> 1) * kN);
+                if ((t & 1) && (t >> 1) >= n_whole) mbar_arrive(loading + ((t >> 1) - n_whole) % Cfg::kCleanRing);
             }
             if (!ok) signal_abort();
             // The last copies have landed before the block may exit.
@@ -323,7 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         issue_s(j + 1, rt);
                     }
-                    ok = wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim);
+                    if (rt == 0 && j >= n_whole) {
+                        const int u = j - n_whole;
+                        ok = wait_warp(clean + u % Cfg::kCleanRing, (uint32_t)(u / Cfg::kCleanRing) & 1u,
+                                       abort_v, lim);
+                    }
+                    ok = ok && wait_warp(p_full + rt, (uint32_t)j & 1u, abort_v, lim);
                     if (!ok) break;
                     tc_fence_after();
                     issue_pv(j, rt);
@@ -337,6 +355,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_one(mma_done, 0, nullptr, lim);
             }
             __syncwarp();
+        }
+        if (warp >= kSoftmaxWarps + 2) {
+            // ------------------------------------------------------ V rows --
+            // Zeros over the V rows of keys that are not read, 64 keys a warp.  (Left
+            // to the softmax, between its P and the product, this took 6 of 43 us
+            // on masked prompts.)
+            const int first = (warp - kSoftmaxWarps - 2) * 64;
+            bool ok = true;
+            uint8_t next[2];
+            auto load_mask = [&](int j) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int key = key0 + j * kN + first + c * 32 + lane;
+                    next[c] = j < n && key < key1 && (!a.mask || a.mask[key] != 0);
+                }
+            };
+            load_mask(n_whole);
+            for (int j = n_whole; ok && j < n; ++j) {
+                uint32_t keys[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) keys[c] = __ballot_sync(0xffffffffu, next[c] != 0);
+                load_mask(j + 1);
+                // Once its copy is on its way the slot's barrier is in this tile's phase
+                // (and stays there until its P V).
+                const int t = 2 * j + 1, i = t % kSlots, u = j - n_whole;
+                ok = wait_warp(loading + u % Cfg::kCleanRing, (uint32_t)(u / Cfg::kCleanRing) & 1u, abort_v,
+                               lim) &&
+                     wait_warp(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim);
+                if (!ok) break;
+                if ((keys[0] & keys[1]) != 0xffffffffu) {
+                    const int c = lane % kChunks;
+#pragma unroll 4
+                    for (int r = lane / kChunks; r < 64; r += 32 / kChunks)
+                        if (!((keys[r >> 5] >> (r & 31)) & 1u))
+                            *reinterpret_cast<uint4 *>(slots + i * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
+                                                       (first + r) * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(clean + u % Cfg::kCleanRing);
+            }
+            if (!ok && lane == 0) signal_abort();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -375,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[c] = j < n && key < key1 && (!a.mask || a.mask[key] != 0);
             }
         };
-        const int n_whole = a.mask ? 0 : (key1 - key0) / kN;  // tiles known to miss none
         uint8_t next[4] = {0, 0, 0, 0};
         if (n_whole == 0) load_mask(0, next);
         for (int j = 0; used && j < n; ++j) {
@@ -464,21 +524,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_wait_st();
-            }
-            // This thread's key's V row, if it is not read.  The first row tile's
-            // P V, which waits for this, comes before the second's.
-            if (!whole && rt == 0) {
-                const int t = 2 * j + 1, i = t % kSlots;
-                if (!wait_warp(full + i, (uint32_t)(t / kSlots) & 1u, abort_v, lim)) {
-                    ok = false;
-                    break;
-                }
-                if (!((keys[quad] >> lane) & 1u))
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        *reinterpret_cast<uint4 *>(slots + i * Cfg::kTileBytes + (c >> 3) * Cfg::kAtom +
-                                                   row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
             }
             tc_fence_before();
             __syncwarp();
