@@ -27,9 +27,9 @@
 // it came from, and the next S follows P V in the tensor pipe's order.
 //
 // Bound by the chain S -> softmax -> P V -> S of a row tile, of which the tensor
-// cores are busy 45%: 16 requests of 512 x 4096, 16 heads of 128: 273 us, 1006
-// TFLOP/s, 0.61 of the measured bf16 peak; head_dim 64 (32 heads) 450 us, 611 TFLOP/s, where the
-// exponentials of both row tiles take their pipe's whole time.  Tried without gain:
+// cores are busy 45%: 16 requests of 512 x 4096, 16 heads of 128: 272 us, 1011
+// TFLOP/s, 0.61 of the measured bf16 peak; head_dim 64 (32 heads) 436 us, 630
+// TFLOP/s, where the exponentials of both row tiles take their pipe's whole time.  Tried without gain:
 // a part of the exponentials as a polynomial on the FMA pipe (issue slots run out
 // instead), two threads a row (registers spill), P V of a tile's first 96 keys
 // before the rest's P is made, and persistent blocks (the loop's registers).
