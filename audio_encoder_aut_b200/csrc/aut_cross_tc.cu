@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_rt = rows - row0 > kM ? 2 : 1;  // row tiles in use
     const int n_whole = a.mask ? 0 : max(0, key1 - key0) / kN;  // key tiles known to miss no key
 
-            // Q: 16 bytes a thread, rows one after the other; the loads run while the block
+    // Q: 16 bytes a thread, rows one after the other; the loads run while the block
     // sets itself up.
     constexpr int kChunks = HD / 8, kLoads = 2 * kM * kChunks / (32 * kSoftmaxWarps);
     constexpr int kStep = 32 * kSoftmaxWarps / kChunks;  // rows from one load to the next
