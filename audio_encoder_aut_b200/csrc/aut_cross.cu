@@ -470,9 +470,9 @@ aut_status check_shape(int heads_q, int heads_kv, int hd, const int32_t *cu_q, c
     if (cu_q[0] != 0 || cu_k[0] != 0) return AUT_ERR_INVALID_ARG;
     for (int i = 0; i < n_seq; ++i)
         if (cu_q[i + 1] < cu_q[i] || cu_k[i + 1] < cu_k[i]) return AUT_ERR_INVALID_ARG;
-    // Row indexes (query, head of a group) are 32-bit in the kernels, and so are
-    // key indexes, a few tiles past the last key included.
-    if ((int64_t)cu_q[n_seq] * heads_q > 0x7fffffffll || cu_k[n_seq] > 0x7ffff000)
+    // Row indexes (query, head of a group) and key indexes are 32-bit in the kernels,
+    // a block's spare rows and a few tiles past the last key included.
+    if ((int64_t)cu_q[n_seq] * heads_q > 0x7ffff000 || cu_k[n_seq] > 0x7ffff000)
         return AUT_ERR_UNSUPPORTED;
     return AUT_OK;
 }

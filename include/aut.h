@@ -404,7 +404,8 @@ aut_status aut_qk_norm_rope(const aut_head_rows *q, const aut_head_rows *k, int3
  * (one projection's halves, say); all `dtype` AUT_BF16 or AUT_F16, rows 16-byte
  * aligned; out must not overlap the inputs, and its rows past cu_q[n_seq] and
  * columns past the heads stay as they are.  cu_q, cu_k: HOST int32 [n_seq + 1],
- * non-decreasing from 0.  key_mask: device uint8 [cu_k[n_seq]].  heads_q a
+ * non-decreasing from 0; cu_q[n_seq] * heads_q and cu_k[n_seq] at most 0x7ffff000
+ * (AUT_ERR_UNSUPPORTED beyond).  key_mask: device uint8 [cu_k[n_seq]].  heads_q a
  * multiple of heads_kv; head_dim 16, 32, 64 or 128; scale > 0.
  * Scores, the softmax and the sums are fp32; the probabilities enter the P V
  * product in `dtype`.  workspace: device, 256-byte aligned, at least

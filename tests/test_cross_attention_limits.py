@@ -1,0 +1,21 @@
+"""Cross attention's limits on what it is given, on the host (no GPU is needed)."""
+import numpy as np
+import pytest
+
+from audio_encoder_aut_b200 import _lib as A
+
+P = 1 << 20  # an aligned address that is never read
+MOST = 0x7ffff000
+
+
+@pytest.mark.parametrize("rows,heads", [(MOST + 1, 1), ((1 << 31) - 17, 1), ((1 << 31) - 15, 1), ((1 << 31) - 1, 1), ((1 << 30) - 8, 2)])
+def test_rows_near_2_31_are_refused(rows, heads):
+    """A kernel counts a block's spare rows in 32 bits too: (rows + 255) / 256 must not pass them."""
+    cu_q, cu_k = np.array([0, rows], np.int32), np.array([0, 0], np.int32)
+    assert A.aut_cross_attention_workspace_bytes(heads, heads, 16, cu_q, cu_k) == 0
+    assert A.aut_cross_attention(P, 16 * heads, None, 16 * heads, None, 16 * heads, P, 16 * heads, A.BF16, heads, heads, 16, cu_q, cu_k, None,
+                                 1.0, P, 1 << 30, None, 0, 0) == A.AUT_ERR_UNSUPPORTED
+
+
+def test_the_largest_row_count_is_planned():
+    assert A.aut_cross_attention_workspace_bytes(1, 1, 16, np.array([0, MOST], np.int32), np.array([0, 0], np.int32)) >= 256
