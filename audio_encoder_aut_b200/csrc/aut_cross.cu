@@ -257,12 +257,12 @@ __global__ void __launch_bounds__(W * 32, W == kRowWarps ? 3 : 1)
                 for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        sc[j][2 * i + e] = ex2_approx(sc[j][2 * i + e] - base);
+                        sc[j][2 * i + e] = ex2_approx(sc[j][2 * i + e] - (base - kCrossLift<T>));
                         l[i] += sc[j][2 * i + e];
                     }
             }
-            // O += P V.  P in 16 bits: in [0, 1], off by half a step of its type,
-            // the same rounding the output gets once more.
+            // O += P V.  P in 16 bits: in [0, 1] (fp16: [0, 2^7]), off by half a step
+            // of its type, the same rounding the output gets once more.
 #pragma unroll
             for (int j = 0; j < kKeys / 16; ++j) {
                 const uint32_t pf[4] = {pack2<T>(sc[2 * j][0], sc[2 * j][1]),

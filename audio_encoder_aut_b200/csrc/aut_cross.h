@@ -2,15 +2,25 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace aut {
 
 // Up to kCrossInline requests travel in the kernels' parameters (one launch
 // less); longer lists are uploaded to the workspace.
 constexpr int kCrossInline = 256;
+
+// The kernels' probabilities are 2^(s - reference + lift), which cancels in O / sum.
+// fp16 ends at 2^-24 and weights below half of that would drop out of P V (but not out
+// of the sum, which is fp32): many such weights together are no small part of a long
+// row. Lifted by 2^7 those from 2^-32 of the maximum on count; the tile kernel's
+// reference may be 2^8 too low, and 2^15 is within fp16's range. bf16 has fp32's.
+template <typename T>
+constexpr float kCrossLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 // One request as one kernel sees it; the entry behind the last one only has `item`.
 // Its work items are item .. next item (none, if another kernel handles it):

@@ -5,7 +5,7 @@
 //   inputs' type -> O += P V (fp32, tensor memory), O and the row sums scaled
 //   down when a row's maximum has grown by more than 2^8 since O last was: until
 //   then the old maximum serves as the softmax's reference, which cancels in
-//   O / sum, and P stays at most 2^8.
+//   O / sum, and P stays at most 2^8 (fp16: 2^15).
 //
 // Warp roles (384 threads; two tiles of rows, 256 rows in all, and one split of
 // keys per block):
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the new one in the rare case that it has grown too much.
                 float f = 1.f, sum;
                 while (true) {
-                    const float neg = m == -INFINITY ? 0.f : -m * a.scale_log2e;
+                    const float neg = (m == -INFINITY ? 0.f : -m * a.scale_log2e) + kCrossLift<T>;
                     const float2 neg2 = make_float2(neg, neg);
                     float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};

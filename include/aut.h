@@ -408,7 +408,8 @@ aut_status aut_qk_norm_rope(const aut_head_rows *q, const aut_head_rows *k, int3
  * (AUT_ERR_UNSUPPORTED beyond).  key_mask: device uint8 [cu_k[n_seq]].  heads_q a
  * multiple of heads_kv; head_dim 16, 32, 64 or 128; scale > 0.
  * Scores, the softmax and the sums are fp32; the probabilities enter the P V
- * product in `dtype`.  workspace: device, 256-byte aligned, at least
+ * product in `dtype` (fp16: times 2^7, so that weights from 2^-32 of a row's largest
+ * on count).  workspace: device, 256-byte aligned, at least
  * aut_cross_attention_workspace_bytes(...) for the same arguments; its contents
  * need no preparation, and calls that overlap on the GPU need one each.
  * status and timeout_ms as for aut_linear (a device word for pipeline waits
