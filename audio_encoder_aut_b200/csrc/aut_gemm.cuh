@@ -179,12 +179,13 @@ AUT_DEV void add_bias16(float (&v)[16], const __nv_bfloat16 *bias, int n0) {
 }
 
 // 16 int32 accumulator columns (as tcgen05.ld returns their bits) to fp32, times
-// the row's scale and each column's.
+// the row's scale and each column's.  (Ordinary loads of the scales: the kernel that
+// writes them may still have been running when this one started.)
 AUT_DEV void scale_i8x16(float (&v)[16], float sx, const float *w_scale, int n0) {
     const float4 *wp = reinterpret_cast<const float4 *>(w_scale + n0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float4 w = __ldg(wp + q);
+        const float4 w = wp[q];
         v[4 * q] = __int2float_rn(__float_as_int(v[4 * q])) * sx * w.x;
         v[4 * q + 1] = __int2float_rn(__float_as_int(v[4 * q + 1])) * sx * w.y;
         v[4 * q + 2] = __int2float_rn(__float_as_int(v[4 * q + 2])) * sx * w.z;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool slab = m0 < args.M;  // warp-uniform
             const int n_first = (tile % args.num_n_tiles) * BN + half * HW;
             float sx = 0.f;  // I8: this row's scale
-            if constexpr (I8) sx = m0 + lane < args.M ? __ldg(args.x_scale + m0 + lane) : 0.f;
+            if constexpr (I8) sx = m0 + lane < args.M ? args.x_scale[m0 + lane] : 0.f;
             const uint32_t t_res = tmem_base + ((uint32_t)(quad * 32) << 16) + BN + half * HW;
             t_acc += half * HW;
 #pragma unroll 1
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const size_t end = dst_row + n0 + (args.epi == kEpiBf16GeluSplit ? args.N : 0) + 16;
                     if (!AUT_IN_BOUNDS(end <= args.out_elems, args.status)) continue;
                     if constexpr (I8)
-                        scale_i8x16(v, __ldg(args.x_scale + ((tile / args.num_n_tiles) * CG + (int)rank) * 128 + r),
+                        scale_i8x16(v, args.x_scale[((tile / args.num_n_tiles) * CG + (int)rank) * 128 + r],
                                     args.w_scale, n0);
                     if (!resid) add_bias16(v, args.bias, n0);
                     switch (args.epi) {

@@ -1,6 +1,10 @@
 // The 8-bit integer linear layer's own kernels and entry points: quantising
 // rows (tokens or weight channels) to int8 with a scale each, and the product
 // for a few tokens.  Larger products run on the tcgen05 GEMM (aut_gemm.cuh, I8).
+//
+// Each kernel starts while the one before it ends, and that one may be writing its
+// tokens, scales or weights: coherent loads after the wait, no read-only ones (which
+// ask that the data stays as it is from the kernel's start).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -82,8 +86,7 @@ AUT_DEV uint2 quantise8(const float (&x)[8], float scale, float inv) {
 // W warps per row, 8 / W rows a block; a thread keeps C chunks of 8 elements.
 template <typename T, int W, int C>
 __global__ void __launch_bounds__(kQuantThreads, C == 4 ? 4 : 3) quantize_rows_kernel(
-    const T *__restrict__ x, long long ld, int M, int K, int8_t *__restrict__ q,
-    float *__restrict__ scale) {
+    const T *x, long long ld, int M, int K, int8_t *q, float *scale) {
     __shared__ uint32_t warp_max[kQuantThreads / 32];
     pdl_trigger();
     pdl_wait();
@@ -165,8 +168,8 @@ cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, 
 // has the 16 channels as its rows and 8 tokens as its columns; since the sum over
 // K may run in any order, a lane's 16 consecutive bytes of a row serve as its
 // operand words of two products (the same permutation of K on both sides), so
-// weights and tokens go from global memory to registers in 16-byte loads with no
-// shared memory between.  The warps' int32 sums meet in shared memory: exact, so
+// weights (read once: past L1) and tokens go from global memory to registers in
+// 16-byte loads with no shared memory between.  The warps' int32 sums meet in shared memory: exact, so
 // in any order.  One token, 2048 x 2048: 2.2 us, a launch's latency.
 
 constexpr int kFewThreads = 256;
@@ -184,9 +187,8 @@ AUT_DEV void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t
 // NT: tiles of 8 tokens.
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads) linear_i8_few_kernel(
-    const int8_t *__restrict__ x, const float *__restrict__ x_scale, const int8_t *__restrict__ w,
-    const float *__restrict__ w_scale, const __nv_bfloat16 *__restrict__ bias, void *__restrict__ y,
-    int M, int N, int K, int epi) {
+    const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale,
+    const __nv_bfloat16 *bias, void *y, int M, int N, int K, int epi) {
     __shared__ int part[kFewThreads / 32][NT][8][16 + 1];  // [warp][tile][token][channel]
     pdl_trigger();
     pdl_wait();
@@ -208,13 +210,13 @@ __global__ void __launch_bounds__(kFewThreads) linear_i8_few_kernel(
         for (int u = 0; u < kUnroll; ++u) {
             const int k = k0 + u * kStep;
             const bool in = k + 16 * t < K;
-            a[u][0] = in ? __ldg(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
-            a[u][1] = in ? __ldg(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
+            a[u][0] = in ? __ldcg(reinterpret_cast<const uint4 *>(w0 + k)) : zero;
+            a[u][1] = in ? __ldcg(reinterpret_cast<const uint4 *>(w1 + k)) : zero;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int tok = j * 8 + g;
                 b[u][j] = in && tok < M
-                              ? __ldg(reinterpret_cast<const uint4 *>(x + (size_t)tok * K + k + 16 * t))
+                              ? *reinterpret_cast<const uint4 *>(x + (size_t)tok * K + k + 16 * t)
                               : zero;
             }
         }
