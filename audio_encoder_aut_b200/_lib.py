@@ -3,6 +3,7 @@ every step of the encoder runs in the library's kernels.  Raises when the
 library has not been built; there is no fallback."""
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -306,15 +307,19 @@ def aut_inject_workspace_bytes(L: int) -> int:
 
 def _offsets(values):
     """(address, entries, owner) of int32 offsets for a call: a writable contiguous int32
-    buffer (a numpy array, say) is passed as it is, anything else is copied to one."""
+    buffer (a numpy array, say) is passed as it is, anything else is copied to one.  No
+    entries where a value does not fit."""
     try:
         view = memoryview(values)
         if view.format == "i" and view.ndim == 1 and view.contiguous and not view.readonly and view.shape[0]:
             return ctypes.addressof(c_int32.from_buffer(values)), view.shape[0], values
     except TypeError:  # no buffer
         pass
-    arr = (c_int32 * max(1, len(values)))(*[int(v) for v in values])
-    return ctypes.addressof(arr), len(values), arr
+    try:
+        arr = array.array("i", [int(v) for v in values])
+    except OverflowError:
+        return 0, 0, None
+    return arr.buffer_info()[0], len(arr), arr
 
 
 def aut_quantize_rows(x: int, dtype: int, ld_x: int, M: int, K: int, q: int, scale: int,

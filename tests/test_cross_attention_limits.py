@@ -19,3 +19,15 @@ def test_rows_near_2_31_are_refused(rows, heads):
 
 def test_the_largest_row_count_is_planned():
     assert A.aut_cross_attention_workspace_bytes(1, 1, 16, np.array([0, MOST], np.int32), np.array([0, 0], np.int32)) >= 256
+
+
+@pytest.mark.parametrize("far", [1 << 31, (1 << 32) + 100, -(1 << 32) + 100])
+@pytest.mark.parametrize("make", [list, tuple, np.array])
+def test_offsets_past_32_bits_are_refused(make, far):
+    """Not wrapped to offsets that can be planned for."""
+    size = A.aut_cross_attention_workspace_bytes
+    ok, bad = [0, 100], make([0, far])
+    assert size(4, 2, 64, ok, bad) == 0 and size(4, 2, 64, bad, ok) == 0
+    for cu_q, cu_k in ((ok, bad), (bad, ok)):
+        assert A.aut_cross_attention(P, 256, P, 128, P, 128, P, 256, A.BF16, 4, 2, 64, cu_q, cu_k, None, 0.125, P, 0, None, 0,
+                                     0) == A.AUT_ERR_INVALID_ARG
