@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_i8_few_kernel(
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int kMaxK8 = 131072;         // 127^2 * 131072 < 2^31
+constexpr int kMaxK8 = 131072;         // 127 * 128 * 131072 < 2^31 (128^2 * 131072 is not)
 constexpr int kMaxRows = 0x7ffff000;   // row indexes are 32-bit, a block's spare rows included
 
 }  // namespace

@@ -355,10 +355,10 @@ aut_status aut_quantize_rows(const void *x, int32_t dtype, int64_t ld_x, int32_t
  * w_scale: device fp32 [N]; bias: device bf16 [N] or NULL; xq, wq, w_scale,
  * bias and y 16-byte aligned.  epilogue, status, timeout_ms and flags as for
  * aut_linear (AUT_LINEAR_F16 is refused); the GELU and the residual add work on
- * the scaled sum.  K a multiple of 16, at most 131072 (so that no sum passes
- * int32), N a multiple of 16.  At most 32 rows run on a kernel without
- * pipeline waits, which ignores AUT_LINEAR_SINGLE_CTA and refuses
- * AUT_LINEAR_FAULT_INJECT (AUT_ERR_UNSUPPORTED). */
+ * the scaled sum.  N a multiple of 16; K a multiple of 16, at most 131072: no sum
+ * passes int32, but for one of 131072 times -128 * -128 (aut_quantize_rows writes
+ * no -128).  At most 32 rows run on a kernel without pipeline waits, which ignores
+ * AUT_LINEAR_SINGLE_CTA and refuses AUT_LINEAR_FAULT_INJECT (AUT_ERR_UNSUPPORTED). */
 aut_status aut_linear_i8(const void *xq, const void *x_scale, const void *wq, const void *w_scale,
                          const void *bias, void *y, int32_t M, int32_t N, int32_t K,
                          int32_t epilogue, int32_t *status, int32_t timeout_ms, int32_t flags,
