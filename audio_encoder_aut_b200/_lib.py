@@ -124,6 +124,10 @@ _SIGNATURES = {
                                       c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
                                       c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p,
                                       c_size_t, c_void_p, c_int32, c_void_p]),
+    "aut_cross_attention_ex": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                         c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
+                                         c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p,
+                                         c_size_t, c_void_p, c_int32, c_int32, c_void_p]),
     "aut_cross_attention_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_void_p,
                                                        c_void_p, c_int32]),
     "aut_check": (c_int32, [c_void_p]),
@@ -353,6 +357,22 @@ def aut_cross_attention(q: int, ld_q: int, k: int, ld_k: int, v: int, ld_v: int,
     return lib().aut_cross_attention(q, ld_q, k, ld_k, v, ld_v, out, ld_out, dtype, heads_q,
                                      heads_kv, head_dim, pq, pk, nq - 1, key_mask, scale,
                                      workspace, ws_bytes, status, timeout_ms, stream)
+
+
+CROSS_FAULT_K, CROSS_FAULT_V = 1, 2
+
+
+def aut_cross_attention_ex(q: int, ld_q: int, k: int, ld_k: int, v: int, ld_v: int, out: int,
+                           ld_out: int, dtype: int, heads_q: int, heads_kv: int, head_dim: int,
+                           cu_q, cu_k, key_mask: int | None, scale: float, workspace: int,
+                           ws_bytes: int, status: int | None, timeout_ms: int, flags: int,
+                           stream: int) -> int:
+    (pq, nq, keep_q), (pk, nk, keep_k) = _offsets(cu_q), _offsets(cu_k)
+    if nq != nk or nq < 1:
+        return AUT_ERR_INVALID_ARG
+    return lib().aut_cross_attention_ex(q, ld_q, k, ld_k, v, ld_v, out, ld_out, dtype, heads_q,
+                                        heads_kv, head_dim, pq, pk, nq - 1, key_mask, scale,
+                                        workspace, ws_bytes, status, timeout_ms, flags, stream)
 
 
 def aut_cross_attention_workspace_bytes(heads_q: int, heads_kv: int, head_dim: int, cu_q,

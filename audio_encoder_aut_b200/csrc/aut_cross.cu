@@ -708,6 +708,19 @@ extern "C" aut_status aut_cross_attention(
     void *out, int64_t ld_out, int32_t dtype, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
     const int32_t *cu_q, const int32_t *cu_k, int32_t n_seq, const uint8_t *key_mask, float scale,
     void *workspace, size_t ws_bytes, int32_t *status, int32_t timeout_ms, aut_stream_t stream) {
+    return aut_cross_attention_ex(q, ld_q, k, ld_k, v, ld_v, out, ld_out, dtype, heads_q, heads_kv,
+                                  head_dim, cu_q, cu_k, n_seq, key_mask, scale, workspace, ws_bytes,
+                                  status, timeout_ms, 0, stream);
+}
+
+extern "C" aut_status aut_cross_attention_ex(
+    const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+    void *out, int64_t ld_out, int32_t dtype, int32_t heads_q, int32_t heads_kv, int32_t head_dim,
+    const int32_t *cu_q, const int32_t *cu_k, int32_t n_seq, const uint8_t *key_mask, float scale,
+    void *workspace, size_t ws_bytes, int32_t *status, int32_t timeout_ms, int32_t flags,
+    aut_stream_t stream) {
+    if (flags != 0 && flags != AUT_CROSS_FAULT_K && flags != AUT_CROSS_FAULT_V)
+        return AUT_ERR_INVALID_ARG;
     aut_status st = check_shape(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
     if (st != AUT_OK) return st;
     if ((dtype != AUT_BF16 && dtype != AUT_F16) || timeout_ms < 0 || !(scale > 0.f) ||
@@ -731,6 +744,7 @@ extern "C" aut_status aut_cross_attention(
     const CrossLayout lay = cross_layout(p, head_dim, n_seq);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return AUT_ERR_INVALID_ARG;
     if (ws_bytes < lay.total) return AUT_ERR_WORKSPACE;
+    if (flags && p.items[kTilesKernel] == 0) return AUT_ERR_UNSUPPORTED;  // no wait to run out
     if (tq == 0) return AUT_OK;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -750,6 +764,7 @@ extern "C" aut_status aut_cross_attention(
     a.scale_log2e = (float)((double)scale * 1.4426950408889634);
     a.status = reinterpret_cast<int *>(status);
     a.timeout_ns = timeout_ms ? (unsigned long long)timeout_ms * 1000000ull : 4000ull * 1000000ull;
+    a.left_out = flags == AUT_CROSS_FAULT_K ? 1 : flags == AUT_CROSS_FAULT_V ? 2 : 0;
     a.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + lay.part_ml);
     const bool listed = n_seq > kCrossInline;

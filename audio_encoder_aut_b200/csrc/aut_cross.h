@@ -45,6 +45,7 @@ struct CrossArgs {
     float2 *part_ml;  // that maximum (times scale_log2e) and the sum of 2^(s - max)
     int *status;
     unsigned long long timeout_ns;
+    int left_out;  // tests: 1 + the tile kernel's first block's copy that never starts
     const CrossSeq *seqs;  // in the workspace; null: `inline_seqs`
     CrossSeq inline_seqs[kCrossInline + 1];
 };

@@ -249,11 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(full + i, Cfg::kTileBytes);
+                if (t + 1 != a.left_out || blockIdx.x != 0) {
+                    mbar_arrive_expect_tx(full + i, Cfg::kTileBytes);
 #pragma unroll
-                for (int c = 0; c < HD / 64; ++c)
-                    tma_load_2d(slots + i * Cfg::kTileBytes + c * Cfg::kAtom, t & 1 ? &tm_v : &tm_k,
-                                full + i, hk * HD + 64 * c, key0 + (t >> 1) * kN);
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_2d(slots + i * Cfg::kTileBytes + c * Cfg::kAtom, t & 1 ? &tm_v : &tm_k,
+                                    full + i, hk * HD + 64 * c, key0 + (t >> 1) * kN);
+                }
                 if ((t & 1) && (t >> 1) >= n_whole) mbar_arrive(loading + ((t >> 1) - n_whole) % Cfg::kCleanRing);
             }
             if (!ok) signal_abort();

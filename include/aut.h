@@ -422,6 +422,22 @@ aut_status aut_cross_attention(const void *q, int64_t ld_q, const void *k, int64
                                size_t ws_bytes, int32_t *status, int32_t timeout_ms,
                                aut_stream_t stream);
 
+/* aut_cross_attention with control over its failure path, for tests: flags
+ * AUT_CROSS_FAULT_K or AUT_CROSS_FAULT_V leaves out the first key or value copy of
+ * the prompt kernel's first block, so that the waits behind it run out, the kernel
+ * writes AUT_ERR_TIMEOUT to `status` and returns without that block's rows
+ * (AUT_ERR_UNSUPPORTED for a batch without requests on that kernel); 0 for normal
+ * use. */
+#define AUT_CROSS_FAULT_K 1
+#define AUT_CROSS_FAULT_V 2
+aut_status aut_cross_attention_ex(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                  const void *v, int64_t ld_v, void *out, int64_t ld_out,
+                                  int32_t dtype, int32_t heads_q, int32_t heads_kv,
+                                  int32_t head_dim, const int32_t *cu_q, const int32_t *cu_k,
+                                  int32_t n_seq, const uint8_t *key_mask, float scale,
+                                  void *workspace, size_t ws_bytes, int32_t *status,
+                                  int32_t timeout_ms, int32_t flags, aut_stream_t stream);
+
 /* No passage: a library helper.  Bytes of device workspace aut_cross_attention
  * needs for this batch (0 for arguments it refuses). */
 size_t aut_cross_attention_workspace_bytes(int32_t heads_q, int32_t heads_kv, int32_t head_dim,

@@ -31,3 +31,13 @@ def test_offsets_past_32_bits_are_refused(make, far):
     for cu_q, cu_k in ((ok, bad), (bad, ok)):
         assert A.aut_cross_attention(P, 256, P, 128, P, 128, P, 256, A.BF16, 4, 2, 64, cu_q, cu_k, None, 0.125, P, 0, None, 0,
                                      0) == A.AUT_ERR_INVALID_ARG
+
+
+def test_a_copy_is_left_out_of_prompts_only():
+    arg = dict(q=P, ld_q=256, k=P, ld_k=128, v=P, ld_v=128, out=P, ld_out=256, dtype=A.BF16, heads_q=4, heads_kv=2, head_dim=64,
+               cu_q=[0, 1], cu_k=[0, 500], key_mask=None, scale=0.125, workspace=P, ws_bytes=1 << 30, status=None, timeout_ms=0, stream=0)
+    for flags in (A.CROSS_FAULT_K, A.CROSS_FAULT_V):
+        assert A.aut_cross_attention_ex(**arg, flags=flags) == A.AUT_ERR_UNSUPPORTED
+        assert A.aut_cross_attention_ex(**(arg | dict(cu_q=[0, 0])), flags=flags) == A.AUT_ERR_UNSUPPORTED
+    for flags in (3, 4, -1):
+        assert A.aut_cross_attention_ex(**arg, flags=flags) == A.AUT_ERR_INVALID_ARG
