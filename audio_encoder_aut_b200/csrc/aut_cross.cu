@@ -723,8 +723,9 @@ extern "C" aut_status aut_cross_attention_ex(
         return AUT_ERR_INVALID_ARG;
     aut_status st = check_shape(heads_q, heads_kv, head_dim, cu_q, cu_k, n_seq);
     if (st != AUT_OK) return st;
+    const float scale_log2e = (float)((double)scale * 1.4426950408889634);
     if ((dtype != AUT_BF16 && dtype != AUT_F16) || timeout_ms < 0 || !(scale > 0.f) ||
-        !std::isfinite(scale))
+        !std::isfinite(scale_log2e))
         return AUT_ERR_INVALID_ARG;
     const int64_t tq = cu_q[n_seq], tk = cu_k[n_seq], most = (int64_t)1 << 38;
     const int64_t wq = (int64_t)heads_q * head_dim, wk = (int64_t)heads_kv * head_dim;
@@ -761,7 +762,7 @@ extern "C" aut_status aut_cross_attention_ex(
     a.heads_q = heads_q;
     a.heads_kv = heads_kv;
     a.group = heads_q / heads_kv;
-    a.scale_log2e = (float)((double)scale * 1.4426950408889634);
+    a.scale_log2e = scale_log2e;
     a.status = reinterpret_cast<int *>(status);
     a.timeout_ns = timeout_ms ? (unsigned long long)timeout_ms * 1000000ull : 4000ull * 1000000ull;
     a.left_out = flags == AUT_CROSS_FAULT_K ? 1 : flags == AUT_CROSS_FAULT_V ? 2 : 0;

@@ -406,7 +406,7 @@ aut_status aut_qk_norm_rope(const aut_head_rows *q, const aut_head_rows *k, int3
  * columns past the heads stay as they are.  cu_q, cu_k: HOST int32 [n_seq + 1],
  * non-decreasing from 0; cu_q[n_seq] * heads_q and cu_k[n_seq] at most 0x7ffff000
  * (AUT_ERR_UNSUPPORTED beyond).  key_mask: device uint8 [cu_k[n_seq]].  heads_q a
- * multiple of heads_kv; head_dim 16, 32, 64 or 128; scale > 0.
+ * multiple of heads_kv; head_dim 16, 32, 64 or 128; scale in (0, 2.3e38].
  * Scores, the softmax and the sums are fp32; the probabilities enter the P V
  * product in `dtype` (fp16: times 2^7, so that weights from 2^-32 of a row's largest
  * on count).  workspace: device, 256-byte aligned, at least

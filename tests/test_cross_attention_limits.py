@@ -41,3 +41,10 @@ def test_a_copy_is_left_out_of_prompts_only():
         assert A.aut_cross_attention_ex(**(arg | dict(cu_q=[0, 0])), flags=flags) == A.AUT_ERR_UNSUPPORTED
     for flags in (3, 4, -1):
         assert A.aut_cross_attention_ex(**arg, flags=flags) == A.AUT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale,ok", [(3e38, False), (2.4e38, False), (2.3e38, True), (1e-45, True)])
+def test_a_scale_that_overflows_in_base_2_is_refused(scale, ok):
+    """scale log2(e) has to be finite in fp32: scores of zero would otherwise become NaN."""
+    st = A.aut_cross_attention(P, 256, P, 128, P, 128, P, 256, A.BF16, 4, 2, 64, [0, 1], [0, 100], None, scale, P, 0, None, 0, 0)
+    assert st == (A.AUT_ERR_WORKSPACE if ok else A.AUT_ERR_INVALID_ARG)
