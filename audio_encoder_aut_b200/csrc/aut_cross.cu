@@ -10,7 +10,8 @@
 //
 // cross_rows_kernel: 16 rows (query, head of the group) of one request and key
 // head per block.  With so few rows the work is reading keys and values once (256
-// requests of one token on 780 keys, 16 heads of 128 over 8: 122 us, 6.7 TB/s), so
+// requests of one token on 780 keys, 16 heads of 128 over 8: 122 us for 818 MB, far
+// more than L2 holds, 6.7 TB/s: reads alone pass the measured copy's 6.46), so
 // the block's warps each stream key blocks of their own (block w, w + W, ...)
 // through a private ring of cp.async copies, with no barrier between warps until
 // their results are joined at the end.  A masked key, or one past the end, is
@@ -40,7 +41,7 @@ namespace {
 
 // Small rings, so that three blocks share a SM: most requests of a batch are a step
 // or two long, and a block's start and end are then most of its time (256 requests
-// of 6 to 780 keys: 38 us; 65 us with 32 keys and 3 stages, one block a SM).
+// of 6 to 780 keys: 37 us; 65 us with 32 keys and 3 stages, one block a SM).
 constexpr int kRows = 16;    // rows of one block
 constexpr int kRowWarps = 4;
 // With no more blocks than SMs there is room for twice the warps, and half the
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(W * 32, W == kRowWarps ? 3 : 1)
             if (i == stage) live = keys[i];
         const uint32_t ks = smem_addr(ring + stage * 2 * Cfg::kTile), vs = ks + Cfg::kTile;
         if (live) {
-            // S: 16 rows x 32 keys, four tiles of 8 keys.
+            // S: 16 rows x 16 keys, two tiles of 8 keys.
             float sc[kKeys / 8][4];
 #pragma unroll
             for (int j = 0; j < kKeys / 8; ++j)
@@ -262,7 +263,11 @@ __global__ void __launch_bounds__(W * 32, W == kRowWarps ? 3 : 1)
                     }
             }
             // O += P V.  P in 16 bits: in [0, 1] (fp16: [0, 2^7]), off by half a step
-            // of its type, the same rounding the output gets once more.
+            // of its type, the same rounding the output gets once more: for values
+            // independent of each other the two make an error of at most sqrt(2)
+            // times the output's own (one token: 1.06 to 1.11 times).  A second bf16
+            // term took one token from 4.0 to 4.3 us on 390 keys and from 13.8 to 14.9
+            // us on 15600.
 #pragma unroll
             for (int j = 0; j < kKeys / 16; ++j) {
                 const uint32_t pf[4] = {pack2<T>(sc[2 * j][0], sc[2 * j][1]),
@@ -415,13 +420,16 @@ enum { kRowsKernel = 0, kTilesKernel = 1, kJoin = 2, kLists = 3 };
 // Blocks that the row kernel's splits aim for (three a SM); the fewest keys worth a
 // split of their own; and the keys a split is rounded to (whole steps of the row
 // kernel's four warps; whole tiles).  One token on 15600 keys, 8 key heads of 128:
-// 14.8 us with these, 17.2 us with splits of 512, 22.5 us with one block a SM.
+// 13.9 us with these, 16.0 us with splits of at least 512.  (Aiming for one block a
+// SM, which then has eight warps, takes that single call 11.9 us; batches have not
+// been measured so.)  148 SMs are the B200's: a plan asks no GPU, for the workspace
+// helper needs none.
 constexpr int kRowsTarget = 3 * 148;
 constexpr int kMinChunk[2] = {256, 512};
 constexpr int kUnit[2] = {kRowWarps * kKeys, kCrossTileKeys};
 
 // No request of up to so many keys is split: one block then ends before a second
-// kernel has joined two (390 keys, 16 heads of 64: 4.9 us whole, 6.2 us in two).
+// kernel has joined two (390 keys, 16 heads of 64: 4.0 us whole, 4.8 us in two).
 constexpr int kCrossWhole = 512;
 
 struct CrossPlan {
@@ -449,8 +457,8 @@ Splits split_keys(int nk, int kernel, const CrossPlan &p) {
 
 // Which kernel a request runs on.  One 16-row block is the row kernel's.  Two still
 // are: the second read of the keys (out of L2) costs less than the tile kernel's
-// longer start (16 requests of 1500 keys, 16 heads of 64, 32 rows: 35 us against
-// 46 us; 48 rows of 128: 71 us against 60 us), unless the call runs the tile kernel
+// longer start (16 requests of 1500 keys, 16 heads of 64, 32 rows: 34 us against
+// 44 us; 48 rows of 128: 70 us against 58 us), unless the call runs the tile kernel
 // anyway: a kernel of their own then takes longer (16 prompts, one of them of 29
 // rows: 55 us against 50 us).  On a small call, everything is the row kernel's.
 int kernel_of(int64_t nq, int group, int hd, const CrossPlan &p) {
@@ -488,8 +496,8 @@ int64_t split_items(int kernel, int64_t nq, int group, int heads_kv) {
 // of a few candidates, the one with the least estimated time.  An item takes 3.5 us
 // and 2.05 us a tile of keys (1.95 with head_dim 64), a join 2 us and the partial
 // rows' way to memory and back.  (16 heads of 128 over 8, 512 x 4096: 4 requests
-// take 70 us whole and 90 us in the halves that an even share of the work would
-// ask for, one request 69 us whole.)
+// take 68 us whole, and took 90 us in the halves that an even share of the work would
+// ask for; one request takes 31 us in its splits, and took 69 us whole.)
 int tile_chunk(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
                int n_seq, CrossPlan p) {
     const int group = heads_q / heads_kv, unit = kUnit[kTilesKernel];
@@ -534,8 +542,11 @@ int tile_chunk(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int
 // to 4000 keys, 1 and 16 requests: the row kernel takes 3.3 (4.3 with head_dim
 // 128) and 19 (32) ns for every key of a block, three blocks a SM; the tile kernel
 // 5.2 (7) an item and 1.45 (2) a tile of keys, one item a SM, and 2 for a join.
-// One request, 16 heads of 64, 128 rows: 4.9 against 11.8 us on 400 keys, 25
-// against 18 us on 4000.
+// One request, 16 heads of 64, 128 rows: 4.6 against 10.5 us on 400 keys, 24.2
+// against 16.4 us on 4000.  Of 150 calls (1, 4 and 16 requests of 24 to 512 queries on
+// 100 to 4000 keys, 16 heads of 64 and of 128) 147 take the faster kernel or one
+// within 8% of it, the others one within 20%.  (The constants are not tile_chunk's:
+// those weigh the splits of long calls, these whole calls of about a wave.)
 bool small_call(int heads_q, int heads_kv, int hd, const int32_t *cu_q, const int32_t *cu_k,
                 int n_seq) {
     const int group = heads_q / heads_kv;

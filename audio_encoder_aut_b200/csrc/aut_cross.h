@@ -10,8 +10,11 @@
 
 namespace aut {
 
-// Up to kCrossInline requests travel in the kernels' parameters (one launch
-// less); longer lists are uploaded to the workspace.
+// Up to kCrossInline requests travel in the kernels' parameters; longer lists are
+// uploaded to the workspace, a launch for each kernel that reads one, and blocks then
+// look their item up only once that has ended: 257 requests of one token take 27.7 us
+// on 100 keys each and 39.5 us on 6 to 780, 256 take 26.0 and 36.9 us.  Not more, since
+// every launch, of one request too, carries the whole list (8 KB).
 constexpr int kCrossInline = 256;
 
 // The kernels' probabilities are 2^(s - reference + lift), which cancels in O / sum.

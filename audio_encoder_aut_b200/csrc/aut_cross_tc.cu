@@ -27,12 +27,13 @@
 // it came from, and the next S follows P V in the tensor pipe's order.
 //
 // Bound by the chain S -> softmax -> P V -> S of a row tile, of which the tensor
-// cores are busy 45%: 16 requests of 512 x 4096, 16 heads of 128: 272 us, 1011
-// TFLOP/s, 0.61 of the measured bf16 peak; head_dim 64 (32 heads) 436 us, 630
-// TFLOP/s, where the exponentials of both row tiles take their pipe's whole time.  Tried without gain:
-// a part of the exponentials as a polynomial on the FMA pipe (issue slots run out
-// instead), two threads a row (registers spill), P V of a tile's first 96 keys
-// before the rest's P is made, and persistent blocks (the loop's registers).
+// cores are busy 45%: 16 requests of 512 x 4096, 16 heads of 128: 271 us, 1012
+// TFLOP/s, 0.61 of the measured bf16 peak; head_dim 64 (32 heads) 440 us, 625
+// TFLOP/s, the exponentials' pipe busy 58%, the tensor cores 29%, issue slots 40%:
+// there too no pipe is full, the chain is what is long.  Tried without gain: a part of
+// the exponentials as a polynomial on the FMA pipe, two threads a row (registers
+// spill), P V of a tile's first 96 keys before the rest's P is made, and persistent
+// blocks (the loop's registers).
 //
 // Keys past the request's end or masked out score -inf, and their V rows are
 // zeroed in shared memory (they may hold anything, and 0 * NaN is NaN).
@@ -55,8 +56,9 @@ constexpr int kM = 128, kN = kCrossTileKeys;  // rows of a tile, keys of a tile
 constexpr int kSoftmaxWarps = 8;              // four per row tile
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups
 // Registers a thread: 168 at launch (three warps to a quarter of the register
-// file), of which the third warpgroup gives some to the softmax, whose rows of
-// 128 scores otherwise spill.  256 * 208 + 128 * 80 <= 384 * 168.
+// file), of which the third warpgroup gives some to the softmax, for its rows of 128
+// scores.  256 * 208 + 128 * 80 <= 384 * 168.  (The compiler still reports 36 to 48
+// bytes of spill stores.)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 512;
 

@@ -20,11 +20,11 @@ namespace {
 // ---------------------------------------------------------------- quantise --
 // scale = max |x| (1 / 127), q = rint(x / scale): the row's maximum first, then the
 // row again, so a row is kept in registers between the two (the rest of a row too
-// long for them is read a second time).  Bound by HBM, one read
-// of x and one write of q, as long as an element costs no more than about ten
-// instructions and none on the conversion pipe: the maximum is taken on the bits,
-// two 16-bit elements at a time, and rounding is an addition.  15600 x 5120: 59 us
-// from bf16 (4.1 TB/s), 71 us from fp32 (5.6 TB/s).
+// long for them is read a second time).  One read of x and one write of q; an element
+// costs about ten instructions and none on the conversion pipe: the maximum is taken
+// on the bits, two 16-bit elements at a time, and rounding is an addition.  15600 x
+// 5120: from fp32 64 us (6.2 TB/s), bound by HBM; from bf16 61 us (3.9 TB/s), which is
+// not: a warp has no load in flight while it reduces and stores its row.
 
 constexpr int kQuantThreads = 256;
 
@@ -149,9 +149,9 @@ cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, 
                           static_cast<float *>(scale));
     };
     // All eight warps to a row while there are too few rows to fill the GPU
-    // otherwise (390 x 1024 bf16: 2.1 us); else the fewest that keep it in their
+    // otherwise (390 x 1024 fp32: 2.3 us); else the fewest that keep it in their
     // registers, so that more rows are in flight: fp32 in 4 chunks a thread
-    // (15600 x 1280: 19.2 us, 24.0 us in 8), 16-bit types in 8 (14.4 us, 15.3 us in
+    // (15600 x 1280: 17 to 19 us, 24 us in 8), 16-bit types in 8 (14.4 us, 15.3 us in
     // 4: a row of 1280 then takes two warps and a barrier).
     constexpr int C = sizeof(T) == 4 ? 4 : 8;
     if (M >= 8 * sm_count_cached()) {
@@ -163,14 +163,18 @@ cudaError_t launch_quantize(const void *x, long long ld, int M, int K, void *q, 
 }
 
 // ------------------------------------------------- product for a few tokens --
-// Up to 32 tokens: bound by reading the weights once.  A block takes 16 output
+// Up to 32 tokens: the weights are read once.  A block takes 16 output
 // channels, its eight warps share K in blocks of 64 bytes.  One m16n8k32 product
 // has the 16 channels as its rows and 8 tokens as its columns; since the sum over
 // K may run in any order, a lane's 16 consecutive bytes of a row serve as its
 // operand words of two products (the same permutation of K on both sides), so
 // weights (read once: past L1) and tokens go from global memory to registers in
-// 16-byte loads with no shared memory between.  The warps' int32 sums meet in shared memory: exact, so
-// in any order.  One token, 2048 x 2048: 2.2 us, a launch's latency.
+// 16-byte loads with no shared memory between.  The warps' int32 sums meet in shared
+// memory: exact, so in any order.  One token, 2048 x 2048 in L2: 2.4 us, a launch's
+// latency.  Weights from HBM, N x K: 1 token 13824 x 5120 13.7 us (5.2 TB/s), 5120 x
+// 13824 21.7 us (3.3), 4096 x 4096 7.6 us (2.2).  On 5120 x 13824, 8 tokens take 22.2
+// us, 16 31.6 us and 32 64.4 us (every block reads the tokens anew, with 32 of them
+// twice the weights' bytes in all), where 33 tokens take 38.0 us on the tcgen05 GEMM.
 
 constexpr int kFewThreads = 256;
 constexpr int kFewTokens = 32;
